@@ -18,6 +18,11 @@ the loop that joins them with an all-reduce is clustering_flashassign_b200.dist)
     fk_init_centers(init, centers)              fp32 master copy of the initial centroids
     fk_lloyd_step_partial(x, xn, centers_dt, ids, sums, counts)   assign + unnormalised update
     fk_update_finalize(sums, counts, centers, centers_dt, max_shift)
+
+Soft assignment (clustering_flashassign_b200.soft has the differentiable form):
+
+    fk_logprob(x, c, ids, logp, lse, ...)       token log probabilities, entropy, top alternatives
+    fk_logprob_backward(x, c, ids, lse, ...)    their gradients
 """
 from __future__ import annotations
 
@@ -41,7 +46,8 @@ EXPORTS = ["fk_assign", "fk_update", "fk_sort", "fk_lloyd", "fk_assign_noalloc",
            "fk_status_string",
            "fk_last_error", "fk_device_error", "fk_release", "fk_profile_enable", "fk_profile_read", "fk_profile_timeline",
            "fk_launch_count", "fk_version", "fk_selftest_bounded_wait", "fk_point_norms",
-           "fk_init_centers", "fk_lloyd_step_partial", "fk_update_finalize", "fk_inject_fault"]
+           "fk_init_centers", "fk_lloyd_step_partial", "fk_update_finalize", "fk_inject_fault",
+           "fk_logprob", "fk_logprob_workspace", "fk_logprob_backward", "fk_logprob_backward_workspace"]
 
 
 class FkError(RuntimeError):
@@ -96,6 +102,10 @@ def _load():
                                       ctypes.POINTER(FkOptions)]),
         "fk_update_finalize": (I, [P, P, I, I, I, I, P, P, P, P]),
         "fk_inject_fault": (I, [I, LL]),
+        "fk_logprob": (I, [ctypes.POINTER(FkShape), P, P, P, F, P, P, P, P, I, P, P, P, LL, P]),
+        "fk_logprob_workspace": (I, [ctypes.POINTER(FkShape), I, ctypes.POINTER(LL)]),
+        "fk_logprob_backward": (I, [ctypes.POINTER(FkShape), P, P, P, F, P, P, P, P, P, P, P, P, P, P, LL, P]),
+        "fk_logprob_backward_workspace": (I, [ctypes.POINTER(FkShape), I, I, ctypes.POINTER(LL)]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -256,6 +266,95 @@ def fk_update_finalize(sums: torch.Tensor, counts: torch.Tensor, centers: torch.
         _check(lib.fk_update_finalize(_ptr(sums), _ptr(counts), B, K, d, code, _ptr(centers), _ptr(centers_dt),
                                       _ptr(max_shift), _stream(stream)), "fk_update_finalize")
     return centers
+
+
+def _need(where: str, name: str, t, dtype, shape, device) -> None:
+    """A CUDA tensor of this dtype, shape and device; None passes."""
+    if t is None:
+        return
+    if t.device != device:
+        raise ValueError(f"{where}: {name} is on {t.device}, not on {device}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{where}: {name} must be {dtype} of shape {tuple(shape)}, "
+                         f"got {t.dtype} of shape {tuple(t.shape)}")
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """Caller-owned workspace: torch's allocator ties it to the stream the call runs on
+    (a captured graph keeps its own)."""
+    if stream is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
+def _soft_shape(where, x, c):
+    if not x.is_cuda:
+        raise ValueError(f"{where}: x must be a CUDA tensor")
+    if x.dim() != 3 or c.dim() != 3:
+        raise ValueError(f"{where}: x must be (B, N, d) and c (B, K, d)")
+    (B, N, d), K = x.shape, c.shape[1]
+    code = _dtype_code(x)
+    _need(where, "c", c, x.dtype, (B, K, d), x.device)
+    return FkShape(B, N, K, d, code), B, N, K
+
+
+def fk_logprob(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, logp: torch.Tensor, lse: torch.Tensor,
+               entropy=None, top_ids=None, top_logp=None, bias=None, scale: float = 1.0, workspace=None,
+               stream=None) -> torch.Tensor:
+    """logp[b,n] = s[ids[b,n]] - logsumexp(s), s = scale x.c^T + bias; lse, entropy and the best columns with it.
+
+    x (B,N,d), c (B,K,d), ids (B,N) int32, bias (B,K) fp32; logp / lse / entropy (B,N) fp32,
+    top_ids / top_logp (B,N,top) int32 / fp32.  workspace: a uint8 tensor of at least
+    fk_logprob_workspace bytes (None: allocated here)."""
+    where = "fk_logprob"
+    shape, B, N, K = _soft_shape(where, x, c)
+    dev, f32 = x.device, torch.float32
+    for name, t in (("ids", ids), ("logp", logp), ("lse", lse), ("entropy", entropy)):
+        _need(where, name, t, torch.int32 if name == "ids" else f32, (B, N), dev)
+    _need(where, "bias", bias, f32, (B, K), dev)
+    if (top_ids is None) != (top_logp is None):
+        raise ValueError(f"{where}: top_ids and top_logp come together")
+    top = 0 if top_ids is None else top_ids.shape[-1]
+    _need(where, "top_ids", top_ids, torch.int32, (B, N, top), dev)
+    _need(where, "top_logp", top_logp, f32, (B, N, top), dev)
+    with torch.cuda.device(dev):
+        need = ctypes.c_longlong(0)
+        _check(lib.fk_logprob_workspace(ctypes.byref(shape), top, ctypes.byref(need)), where)
+        ws = workspace if workspace is not None else _scratch(need.value, dev, stream)
+        _need(where, "workspace", ws, torch.uint8, (ws.numel(),), dev)
+        _check(lib.fk_logprob(ctypes.byref(shape), _ptr(x), _ptr(c), _ptr(bias), float(scale), _ptr(ids), _ptr(logp),
+                              _ptr(lse), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logp), _ptr(ws), ws.numel(),
+                              _stream(stream)), where)
+    return logp
+
+
+def fk_logprob_backward(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, lse: torch.Tensor, entropy=None,
+                        dlogp=None, dlse=None, dentropy=None, dx=None, dc=None, dbias=None, bias=None,
+                        scale: float = 1.0, workspace=None, stream=None) -> None:
+    """Gradients of fk_logprob into dx (B,N,d), dc (B,K,d) (x's dtype) and dbias (B,K) fp32, each optional,
+    from upstream gradients dlogp, dlse, dentropy (B,N) fp32, each optional."""
+    where = "fk_logprob_backward"
+    shape, B, N, K = _soft_shape(where, x, c)
+    dev, f32 = x.device, torch.float32
+    for name, t in (("ids", ids), ("lse", lse), ("entropy", entropy), ("dlogp", dlogp), ("dlse", dlse),
+                    ("dentropy", dentropy)):
+        _need(where, name, t, torch.int32 if name == "ids" else f32, (B, N), dev)
+    _need(where, "dx", dx, x.dtype, x.shape, dev)
+    _need(where, "dc", dc, x.dtype, c.shape, dev)
+    _need(where, "bias", bias, f32, (B, K), dev)
+    _need(where, "dbias", dbias, f32, (B, K), dev)
+    with torch.cuda.device(dev):
+        need = ctypes.c_longlong(0)
+        _check(lib.fk_logprob_backward_workspace(ctypes.byref(shape), int(bias is not None), int(dbias is not None),
+                                                 ctypes.byref(need)), where)
+        ws = workspace if workspace is not None else _scratch(need.value, dev, stream)
+        _need(where, "workspace", ws, torch.uint8, (ws.numel(),), dev)
+        _check(lib.fk_logprob_backward(ctypes.byref(shape), _ptr(x), _ptr(c), _ptr(bias), float(scale), _ptr(ids),
+                                       _ptr(lse), _ptr(entropy), _ptr(dlogp), _ptr(dlse), _ptr(dentropy), _ptr(dx),
+                                       _ptr(dc), _ptr(dbias), _ptr(ws), ws.numel(), _stream(stream)), where)
 
 
 def fk_device_error(stream=None) -> int:

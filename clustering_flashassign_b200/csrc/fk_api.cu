@@ -21,33 +21,6 @@ int check_shape(int B, long long N, int K, int d, int dtype) {
   return FK_OK;
 }
 
-namespace {
-
-enum Loc { LOC_DEVICE, LOC_HOST_PINNED, LOC_HOST_PAGEABLE };
-
-Loc locate(const void *p) {
-  cudaPointerAttributes at;
-  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return LOC_HOST_PAGEABLE;
-  }
-  if (at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged) return LOC_DEVICE;
-  if (at.type == cudaMemoryTypeHost) return LOC_HOST_PINNED;
-  return LOC_HOST_PAGEABLE;
-}
-
-// Options with the environment's defaults: FK_VERBOSE=1 turns the per-iteration
-// line on, FK_CHUNK_POINTS sets the streamed chunk size when the caller left it 0.
-fk_options options_of(const fk_options *opts) {
-  fk_options o{FK_HOST_AUTO, 0, 0};
-  if (opts) o = *opts;
-  if (const char *e = getenv("FK_VERBOSE"))
-    if (atoi(e) != 0) o.verbose = 1;
-  if (o.chunk_points <= 0)
-    if (const char *e = getenv("FK_CHUNK_POINTS")) o.chunk_points = atoll(e);
-  return o;
-}
-
 int check_ptr(const void *p, const char *name, bool aligned16) {
   if (!p) return set_error(FK_EINVAL, std::string(name) + " is NULL");
   if (aligned16 && (reinterpret_cast<uintptr_t>(p) & 15u))
@@ -75,6 +48,33 @@ int check_dev(const void *p, const char *name) {
 }
 
 int check_dev_opt(const void *p, const char *name) { return p ? check_dev(p, name) : FK_OK; }
+
+namespace {
+
+enum Loc { LOC_DEVICE, LOC_HOST_PINNED, LOC_HOST_PAGEABLE };
+
+Loc locate(const void *p) {
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return LOC_HOST_PAGEABLE;
+  }
+  if (at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged) return LOC_DEVICE;
+  if (at.type == cudaMemoryTypeHost) return LOC_HOST_PINNED;
+  return LOC_HOST_PAGEABLE;
+}
+
+// Options with the environment's defaults: FK_VERBOSE=1 turns the per-iteration
+// line on, FK_CHUNK_POINTS sets the streamed chunk size when the caller left it 0.
+fk_options options_of(const fk_options *opts) {
+  fk_options o{FK_HOST_AUTO, 0, 0};
+  if (opts) o = *opts;
+  if (const char *e = getenv("FK_VERBOSE"))
+    if (atoi(e) != 0) o.verbose = 1;
+  if (o.chunk_points <= 0)
+    if (const char *e = getenv("FK_CHUNK_POINTS")) o.chunk_points = atoll(e);
+  return o;
+}
 
 // An argument that may be host or device memory: device memory must be this device's.
 int check_if_dev(const void *p, Loc where, const char *name) {
@@ -706,7 +706,8 @@ int fk_device_error(fk_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Workspace *ws;
   FK_TRY(workspace_for(s, &ws));
-  return read_device_error(ws, s);
+  FK_TRY(read_device_error(ws, s));
+  return read_soft_error(s);
 }
 
 int fk_release(void) {

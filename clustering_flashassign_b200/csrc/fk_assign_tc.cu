@@ -779,15 +779,13 @@ int get_encoder(EncodeTiledFn *out) {
   return FK_OK;
 }
 
-// (inner, rows, B) tensor of dtype's elements (fp32 for FK_F32, else 16-bit),
-// box (box_inner, box_rows, 1).
-int encode_3d(CUtensorMap *map, const void *base, int dtype, int inner, long long rows, int B,
-              int box_inner, int box_rows, CUtensorMapSwizzle swz) {
+int encode_strided(CUtensorMap *map, const void *base, int dtype, long long inner, long long rows, long long depth,
+                   long long pitch, long long stride, int box_inner, int box_rows, CUtensorMapSwizzle swz) {
   EncodeTiledFn enc;
   FK_TRY(get_encoder(&enc));
   const cuuint64_t es = dtype == FK_F32 ? 4 : 2;
-  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)B};
-  cuuint64_t strides[2] = {(cuuint64_t)inner * es, (cuuint64_t)rows * inner * es};
+  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)depth};
+  cuuint64_t strides[2] = {(cuuint64_t)pitch * es, (cuuint64_t)stride * es};
   cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType ty = dtype == FK_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
@@ -798,6 +796,13 @@ int encode_3d(CUtensorMap *map, const void *base, int dtype, int inner, long lon
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return set_error(FK_ECUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
   return FK_OK;
+}
+
+// (inner, rows, B) tensor of dtype's elements (fp32 for FK_F32, else 16-bit),
+// box (box_inner, box_rows, 1).
+int encode_3d(CUtensorMap *map, const void *base, int dtype, int inner, long long rows, int B,
+              int box_inner, int box_rows, CUtensorMapSwizzle swz) {
+  return encode_strided(map, base, dtype, inner, rows, B, inner, rows * inner, box_inner, box_rows, swz);
 }
 
 template <typename T, bool RESIDENT, int KB, int STAGES>
@@ -822,6 +827,12 @@ int launch_typed(const CUtensorMap &tmx, const CUtensorMap &tmc, const TcArgs &a
 }
 
 }  // namespace
+
+int encode_tiles(void *map, const void *base, int dtype, long long inner, long long rows, long long depth,
+                 long long pitch, long long stride, int box_inner, int box_rows) {
+  return encode_strided(static_cast<CUtensorMap *>(map), base, dtype, inner, rows, depth, pitch, stride, box_inner,
+                        box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 
 int launch_point_norms(const void *x, int dtype, long long rows, int d, float *xn, cudaStream_t s) {
   if (dtype == FK_BF16) return point_norms_t<__nv_bfloat16>(x, rows, d, xn, s);

@@ -121,6 +121,24 @@ int num_sms();
 // K > 2^24.
 int check_shape(int B, long long N, int K, int d, int dtype);
 
+// Pointer rules shared by the entry points: FK_EINVAL for NULL, for an address
+// that is not 16-byte aligned (where asked for), and for what is not memory of
+// the current device (managed memory is accepted).
+int check_ptr(const void *p, const char *name, bool aligned16);
+int check_dev(const void *p, const char *name);
+int check_dev_opt(const void *p, const char *name);
+
+// The soft assignment operators take their scratch from the caller, so that a
+// captured graph owns what it replays on; their device error word is one
+// static word per device.  read_soft_error synchronizes `s`, reads and clears it.
+int soft_error_word(int **out);
+int read_soft_error(cudaStream_t s);
+
+// Tensor map with the 128-byte swizzle: (inner, rows, depth) elements of dtype,
+// row pitch and depth stride in elements, box (box_inner, box_rows, 1).
+int encode_tiles(void *map, const void *base, int dtype, long long inner, long long rows, long long depth,
+                 long long pitch, long long stride, int box_inner, int box_rows);
+
 // Programmatic dependent launch: the kernels of one Lloyd iteration are
 // launched so that each may start while its predecessor in the stream drains.
 // A kernel launched this way calls pdl_wait() before it reads anything an

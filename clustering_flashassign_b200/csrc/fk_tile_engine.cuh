@@ -1,0 +1,367 @@
+// Tile engine of the soft assignment operators: a persistent, warp-specialised
+// product of two 16-bit operands on tcgen05, whose epilogue is a template
+// argument.  It serves
+//   scores   S = X C^T        both operands with the contraction (d) contiguous,
+//   dX       G C              C has its rows along the contraction ("MN-major"),
+//   dC       G^T X            both operands have their rows along the contraction.
+//
+// One tile is 128 * CG rows by 256 columns: CG = 2 pairs two SMs on one tile
+// (cta_group::2; each CTA stages its own 128 rows and half of the columns, so
+// a K-block costs each SM 32 KB of operand traffic per 512 tensor cycles
+// instead of the 48 KB of a lone CTA, which L2 cannot feed to all SMs).
+//
+//   warp 0      TMA producer (one thread): 64-wide K-blocks of both operands
+//               into 128-byte-swizzled stages,
+//   warp 1      one thread (of the pair's first CTA) issues tcgen05.mma,
+//               M = 128 * CG, N = 256, K = 16; two 256-column accumulators in
+//               TMEM let the next tile's products overlap this tile's epilogue,
+//   warps 2..9  epilogue: two warps share each 32-row quadrant and split the
+//               tile's columns in halves.
+//
+// fp32 operands come as three bf16 planes (hi, mid, lo: 8 + 8 + 8 significant
+// bits) and the contraction runs over the six plane pairs whose product is
+// above 2^-24 of the leading one, smallest first.  That costs 6 bf16 products,
+// exactly the tensor time of three TF32 ones at half the rate, keeps fp32's
+// range, and needs no second set of layouts (TF32 operands cannot be read
+// MN-major).
+//
+// Work: a unit is one row tile against a run of consecutive column tiles (or
+// one tile over a part of the contraction).  Units are numbered so that those
+// in flight together cover one group of row tiles against the same columns:
+// the columns' operand is read from HBM about once per group, and the group's
+// rows stay in L2.
+#pragma once
+
+#include "fk_sm100.cuh"
+
+namespace fk {
+namespace tile {
+
+using namespace sm100;
+
+constexpr int kRows = 128;   // rows of one CTA's tile
+constexpr int kCols = 256;   // columns of a tile
+constexpr int kK = 64;       // contraction elements per stage
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr uint32_t kABytes = kRows * kK * 2;
+constexpr int kMaxStages = 8;
+constexpr int kCtrlBytes = 256;  // barriers, TMEM address, abort flag
+
+template <int CG>
+struct Geo {
+  static constexpr uint32_t kBBytes = kCols / CG * kK * 2;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes;
+};
+
+struct Plan {
+  int units;        // B * ksplits * runs * row_tiles
+  int row_tiles;    // tiles of 128 * CG rows
+  int col_tiles;
+  int runs;         // column runs per row tile
+  int ksplits;      // parts of the contraction
+  int group;        // row tiles per group
+  int kblocks;      // 64-wide blocks of one plane pair
+  int pairs;        // 1, or 6 for fp32
+  int planes;       // 1, or 3
+  int stages;
+  uint32_t idesc;
+};
+
+struct Unit {
+  int b, rt, ct0, ct1, k0, k1, run, ks;
+};
+
+__host__ __device__ __forceinline__ Unit unit_of(const Plan &p, int u) {
+  Unit w;
+  const int per_b = p.ksplits * p.runs * p.row_tiles;
+  w.b = u / per_b;
+  int r = u - w.b * per_b;
+  const int full = p.ksplits * p.runs * p.group;
+  const int g = r / full;
+  r -= g * full;
+  const int rows = p.row_tiles - g * p.group < p.group ? p.row_tiles - g * p.group : p.group;
+  const int q = r / rows;
+  w.rt = g * p.group + (r - q * rows);
+  w.ks = q / p.runs;
+  w.run = q - w.ks * p.runs;
+  w.ct0 = (int)((long long)w.run * p.col_tiles / p.runs);
+  w.ct1 = (int)((long long)(w.run + 1) * p.col_tiles / p.runs);
+  const long long kt = (long long)p.pairs * p.kblocks;
+  w.k0 = (int)(w.ks * kt / p.ksplits);
+  w.k1 = (int)((w.ks + 1) * kt / p.ksplits);
+  return w;
+}
+
+// The plane pair of a contraction step, smallest products first.
+__device__ __forceinline__ void pair_planes(int pairs, int pair, int &pa, int &pb) {
+  if (pairs == 1) {
+    pa = pb = 0;
+    return;
+  }
+  // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
+  pa = (0x001012 >> (4 * pair)) & 15;
+  pb = (0x010210 >> (4 * pair)) & 15;
+}
+
+// Descriptor of an operand whose contraction index is the row of the tile:
+// blocks of 64 columns (128 bytes, 128-byte swizzle) by 64 rows; 8-row groups
+// 1024 bytes apart, the next 64 columns one block (8 KB) further.  16 rows
+// (one MMA step) are 2048 bytes.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
+  uint64_t desc = 0;
+  desc |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  desc |= (uint64_t)(8192u >> 4) << 16;
+  desc |= (uint64_t)(1024u >> 4) << 32;
+  desc |= (uint64_t)1u << 46;
+  desc |= (uint64_t)2u << 61;
+  return desc;
+}
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (CG == 1) {
+    mma_f16(d, a, b, idesc, acc);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  }
+}
+
+// Commit of the MMAs issued so far: one arrival on `bar` of every CTA of the pair.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 1) {
+    mma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            bar),
+        "h"((uint16_t)3)
+        : "memory");
+  }
+}
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// Tiled load whose bytes are counted on a barrier of the pair's first CTA
+// (bar: a shared::cluster address).
+template <int CG>
+__device__ __forceinline__ void load_3d(const CUtensorMap *map, uint32_t dst, uint32_t bar, int c0, int c1, int c2) {
+  if constexpr (CG == 1) {
+    tma_load_3d(map, dst, bar, c0, c1, c2);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc_cg(uint32_t dst, uint32_t n) {
+  if constexpr (CG == 1) {
+    tmem_alloc(dst, n);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(n) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc_cg(uint32_t addr, uint32_t n) {
+  if constexpr (CG == 1) tmem_dealloc(addr, n);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(n) : "memory");
+}
+
+// All lanes return the same verdict of a wait that lane 0 polls.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
+                                          int lane) {
+  int ok = 1;
+  if (lane == 0) ok = mbar_wait_spin(bar, parity, abort_flag, err);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// What an epilogue sees.  Epi provides
+//   struct Args                                 kernel argument
+//   static size_t smem_bytes                    (host side, own dynamic shared memory)
+//   begin(const Unit &)                         at the unit's first tile
+//   tile(tmem address of this warp's 32 rows and first column, column tile)
+//   end(const Unit &)                           after the unit's last tile
+// and is constructed per thread with (args, lane, row in CTA tile, half, shared memory).
+template <int CG, bool A_MN, bool B_MN, class Epi>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_tiles(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+            const __grid_constant__ Plan p, const __grid_constant__ typename Epi::Args ea, int *err) {
+  extern __shared__ uint8_t smem_raw[];
+  using G = Geo<CG>;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t *gen = smem_raw + (base - smem_u32(smem_raw));
+  const uint32_t ctrl = base + p.stages * G::kStageBytes;
+  uint8_t *ctrl_gen = gen + p.stages * G::kStageBytes;
+  auto full = [&](int s) { return ctrl + 8u * s; };
+  auto empty = [&](int s) { return ctrl + 64u + 8u * s; };
+  auto tfull = [&](int i) { return ctrl + 128u + 8u * i; };
+  auto tempty = [&](int i) { return ctrl + 144u + 8u * i; };
+  const uint32_t tmem_slot = ctrl + 160u;
+  volatile int *abort_flag = reinterpret_cast<int *>(ctrl_gen + 164);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 1 ? 0u : cta_rank();
+  const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull(i), 1);
+      mbar_init(tempty(i), kEpiWarps * CG);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&ta);
+    prefetch_tensormap(&tb);
+  }
+  if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // the pair's barriers exist before anyone signals them
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctrl_gen + 160);
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = worker; u < p.units && ok; u += workers) {
+        const Unit w = unit_of(p, u);
+        const int arow = (w.rt * CG + (int)rank) * kRows;
+        for (int ct = w.ct0; ct < w.ct1 && ok; ++ct) {
+          const int bcol = ct * kCols + (int)rank * (kCols / CG);
+          for (int k = w.k0; k < w.k1; ++k, ++it) {
+            const int s = it % p.stages;
+            if (!mbar_wait_spin(empty(s), ((it / p.stages) & 1) ^ 1, abort_flag, err)) { ok = false; break; }
+            const int pair = k / p.kblocks, kb = k - pair * p.kblocks;
+            int pa, pb;
+            pair_planes(p.pairs, pair, pa, pb);
+            pa += w.b * p.planes;
+            pb += w.b * p.planes;
+            const uint32_t sa = base + s * G::kStageBytes, sb = sa + kABytes;
+            const uint32_t bar = CG == 1 ? full(s) : map_to_cta(full(s), 0);
+            if (rank == 0) mbar_arrive_expect_tx(full(s), G::kStageBytes * CG);
+            if constexpr (A_MN) {
+#pragma unroll
+              for (int i = 0; i < kRows / 64; ++i)
+                load_3d<CG>(&ta, sa + i * 8192u, bar, arow + i * 64, kb * kK, pa);
+            } else {
+              load_3d<CG>(&ta, sa, bar, kb * kK, arow, pa);
+            }
+            if constexpr (B_MN) {
+#pragma unroll
+              for (int i = 0; i < kCols / CG / 64; ++i)
+                load_3d<CG>(&tb, sb + i * 8192u, bar, bcol + i * 64, kb * kK, pb);
+            } else {
+              load_3d<CG>(&tb, sb, bar, kb * kK, bcol, pb);
+            }
+          }
+        }
+      }
+      // leave only when the issued copies have landed: every stage was handed
+      // back by the MMA (bounded; after an abort the copies get a millisecond)
+      if (ok) {
+        const uint32_t n = it < (uint32_t)p.stages ? it : (uint32_t)p.stages;
+        for (uint32_t j = it - n; j < it; ++j)
+          if (!mbar_wait_spin(empty(j % p.stages), (j / p.stages) & 1, abort_flag, err)) { ok = false; break; }
+      }
+      if (!ok) {
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) {}
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (int u = worker; u < p.units && ok; u += workers) {
+        const Unit w = unit_of(p, u);
+        for (int ct = w.ct0; ct < w.ct1 && ok; ++ct, ++n) {
+          const uint32_t buf = n & 1;
+          if (!mbar_wait_spin(tempty(buf), ((n >> 1) & 1) ^ 1, abort_flag, err)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t d = tmem + buf * kCols;
+          for (int k = w.k0; k < w.k1; ++k, ++it) {
+            const int s = it % p.stages;
+            if (!mbar_wait_spin(full(s), (it / p.stages) & 1, abort_flag, err)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = base + s * G::kStageBytes, sb = sa + kABytes;
+#pragma unroll
+            for (int kk = 0; kk < kK / 16; ++kk) {
+              const uint64_t da = A_MN ? desc_mn_sw128(sa + kk * 2048u) : desc_k_sw128(sa + kk * 32u);
+              const uint64_t db = B_MN ? desc_mn_sw128(sb + kk * 2048u) : desc_k_sw128(sb + kk * 32u);
+              mma<CG>(d, da, db, p.idesc, k > w.k0 || kk > 0);
+            }
+            commit<CG>(empty(s));
+          }
+          if (ok) commit<CG>(tfull(buf));
+        }
+      }
+    }
+  } else {
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    Epi epi(ea, lane, quad * 32 + lane, half, ctrl_gen + kCtrlBytes);
+    uint32_t n = 0;
+    bool ok = true;
+    for (int u = worker; u < p.units && ok; u += workers) {
+      const Unit w = unit_of(p, u);
+      epi.begin(w, (w.rt * CG + (int)rank) * kRows);
+      for (int ct = w.ct0; ct < w.ct1; ++ct, ++n) {
+        const uint32_t buf = n & 1;
+        if (!warp_wait(tfull(buf), (n >> 1) & 1, abort_flag, err, lane)) { ok = false; break; }
+        tc_fence_after();
+        epi.tile(tmem + buf * kCols + half * (kCols / 2) + ((uint32_t)(quad * 32) << 16),
+                 (long long)ct * kCols + half * (kCols / 2));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 1 || rank == 0) mbar_arrive(tempty(buf));
+          else arrive_cluster(map_to_cta(tempty(buf), 0));
+        }
+      }
+      if (ok) epi.end(w);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_cg<CG>(tmem, 512);
+  }
+}
+
+}  // namespace tile
+}  // namespace fk

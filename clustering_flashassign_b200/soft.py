@@ -1,0 +1,93 @@
+"""Soft assignment over libfk: token log probabilities and their gradients.
+
+    r = token_log_probs(x, c, ids, top=5)
+    r.logp, r.lse, r.entropy, r.top_ids, r.top_logp
+
+The soft form of the hard assignment: where fk_assign picks the nearest entry of a
+table for every row, this gives the log probability of a given entry (token, cluster)
+under the softmax of the row's scores, with the entropy of that distribution and its
+likeliest entries, without storing the scores.  It differentiates with respect to the
+rows, the table and the bias.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import fk_logprob, fk_logprob_backward
+
+
+class TokenLogProbs(NamedTuple):
+    logp: torch.Tensor                 # log probability of the given id (0 where the id is negative)
+    lse: torch.Tensor                  # log of the sum of exp(score)
+    entropy: torch.Tensor              # of the row's distribution
+    top_ids: Optional[torch.Tensor]    # likeliest entries, int32, or None with top = 0
+    top_logp: Optional[torch.Tensor]
+
+
+class _LogProbs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, c, bias, ids, scale, top):
+        B, N, _ = x.shape
+        row = dict(dtype=torch.float32, device=x.device)
+        logp, lse, entropy = torch.empty(3, B, N, **row).unbind(0)
+        top_ids = torch.empty((B, N, top), dtype=torch.int32, device=x.device) if top else None
+        top_logp = torch.empty((B, N, top), **row) if top else None
+        fk_logprob(x, c, ids, logp, lse, entropy, top_ids, top_logp, bias, scale)
+        ctx.save_for_backward(x, c, bias, ids, lse, entropy)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        if top:
+            ctx.mark_non_differentiable(top_ids, top_logp)
+        return logp, lse, entropy, top_ids, top_logp
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogp, dlse, dentropy, *_):
+        x, c, bias, ids, lse, entropy = ctx.saved_tensors
+        up = [None if g is None else g.float().contiguous() for g in (dlogp, dlse, dentropy)]
+        if all(g is None for g in up):
+            return (None,) * 6
+        want = ctx.needs_input_grad
+        dx = torch.empty_like(x) if want[0] else None
+        dc = torch.empty_like(c) if want[1] else None
+        dbias = torch.empty_like(bias) if want[2] else None
+        fk_logprob_backward(x, c, ids, lse, entropy, *up, dx, dc, dbias, bias, ctx.scale)
+        return dx, dc, dbias, None, None, None
+
+
+def token_log_probs(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0,
+                    bias: torch.Tensor | None = None, top: int = 0) -> TokenLogProbs:
+    """Log probabilities of ids under softmax(scale * x c^T + bias), with entropy and alternatives.
+
+    x (..., d) with one table c (K, d) and ids (...), or batches x (B, N, d), c (B, K, d),
+    ids (B, N); fp16, bf16 (d a multiple of 8) or fp32, x and c alike.  ids int32 or int64,
+    negative: ignored (log probability 0, no gradient from it).  bias (K,) or (B, K);
+    -inf masks an entry.  top <= min(K, 28) likeliest entries, lowest index on ties.
+    logp, lse and entropy are fp32 and differentiable; top_ids and top_logp are not.
+    """
+    if x.dim() < 1 or c.dim() not in (2, 3):
+        raise ValueError("x must be (..., d) and c (K, d), or x (B, N, d) and c (B, K, d)")
+    lead = tuple(x.shape[:-1])
+    if tuple(ids.shape) != lead:
+        raise ValueError(f"ids must be {lead}, got {tuple(ids.shape)}")
+    if ids.dtype == torch.int64:  # any value out of range stays out of range
+        ids = ids.clamp(-1, c.shape[-2])
+    elif ids.dtype != torch.int32:
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    if bias is not None:
+        bias = bias.float()
+    if c.dim() == 2:
+        xs, cs, ids = x.reshape(1, -1, x.shape[-1]), c.unsqueeze(0), ids.reshape(1, -1)
+        if bias is not None:
+            bias = bias.unsqueeze(0)
+    else:
+        xs, cs = x, c
+    if bias is not None:
+        bias = bias.contiguous()
+    out = _LogProbs.apply(xs.contiguous(), cs.contiguous(), bias, ids.int().contiguous(), float(scale), int(top))
+    if c.dim() == 2:
+        out = [None if t is None else t.reshape(lead + tuple(t.shape[2:])) for t in out]
+    return TokenLogProbs(*out)

@@ -309,6 +309,57 @@ int fk_assign_noalloc(const void *x, const void *c, int B, long long N, int K, i
  */
 int fk_noalloc_device_error(fk_stream_t stream);
 
+/*
+ * fk_logprob -- token log probabilities: the soft form of fk_assign.  Rows x
+ * (B, N, d) meet a table c (B, K, d) (a vocabulary, a codebook, centroids):
+ *     s[b,n,k] = scale * x[b,n] . c[b,k] + bias[b,k]
+ *     lse      = log sum_k exp(s)                     (B, N) fp32
+ *     logp     = s[b,n,ids[b,n]] - lse                (B, N) fp32
+ *     entropy  = -sum_k p log p, p = exp(s - lse)     (B, N) fp32, nullable
+ *     top_ids, top_logp  the `top` largest s, lowest index on ties (ordered by
+ *                        their value in fp64), and their log probabilities
+ *                        (B, N, top); NULL with top = 0
+ * The (B, N, K) scores are never stored.  For -t ||x - c||^2 in place of the
+ * product pass scale = 2 t and bias = -t ||c||^2 (the row's own norm drops out).
+ *
+ * shape: N >= 0 (K may exceed N), d <= 2^20, otherwise fk_assign's rules.
+ * scale positive and finite.  bias fp32 (B, K), nullable; an entry of -inf masks
+ * its column whatever the table's row holds.  0 <= top <= min(K, 28).  A negative
+ * id is ignored: its logp is 0.  An id of K or more does the same and records
+ * FK_EINVAL in the device error word.  A row whose every column is masked has
+ * lse = logp = -inf and entropy 0; masked columns fill up top, lowest index
+ * first.  fp32 inputs are multiplied as three bf16 parts each (about 2^-24).
+ *
+ * workspace: device memory of the caller's (16-byte aligned, at least
+ * fk_logprob_workspace bytes), in use until the call's work on `stream` is
+ * done; calls in flight at once, and captured graphs that may be, each need
+ * their own.  Nothing is allocated.
+ */
+int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float *bias, float scale,
+               const int32_t *ids, float *logp, float *lse, float *entropy, int top, int32_t *top_ids,
+               float *top_logp, void *workspace, long long workspace_bytes, fk_stream_t stream);
+int fk_logprob_workspace(const fk_shape *shape, int top, long long *bytes);
+
+/*
+ * fk_logprob_backward -- gradients of fk_logprob for upstream gradients dlogp,
+ * dlse, dentropy (B, N) fp32 (each nullable):
+ *     G    = dlogp (1[k = id] - p) + dlse p - dentropy p (log p + entropy)
+ *     dx   = scale G c        (B, N, d) in the inputs' type
+ *     dc   = scale G^T x      (B, K, d) in the inputs' type
+ *     dbias = sum_n G         (B, K) fp32
+ * Each result is nullable (not computed).  lse and entropy are the forward
+ * call's (entropy only with dentropy).  Ignored rows get nothing from dlogp; a
+ * row without any upstream gradient gets zeros and contributes nothing, whatever
+ * it holds; masked columns get zeros and contribute nothing.  Results are
+ * bit-reproducible: no atomics touch them.  Workspace as in fk_logprob; it holds
+ * G in the inputs' type for a block of rows, 4 GiB at most (256 rows at least).
+ */
+int fk_logprob_backward(const fk_shape *shape, const void *x, const void *c, const float *bias, float scale,
+                        const int32_t *ids, const float *lse, const float *entropy, const float *dlogp,
+                        const float *dlse, const float *dentropy, void *dx, void *dc, float *dbias,
+                        void *workspace, long long workspace_bytes, fk_stream_t stream);
+int fk_logprob_backward_workspace(const fk_shape *shape, int with_bias, int with_dbias, long long *bytes);
+
 /* Static text for a status code. */
 const char *fk_status_string(int status);
 
@@ -320,7 +371,9 @@ const char *fk_last_error(void);
  * workspace.  Returns FK_OK, FK_ETIMEOUT (a bounded wait in a kernel gave
  * up), FK_EUNSUPPORTED (an fp16 squared norm of 2^32 or more reached the
  * tensor-core assign's norm digits) or FK_EINVAL (an id outside [0, K)
- * reached fk_update / fk_sort).
+ * reached fk_update / fk_sort).  The soft assignment operators (fk_logprob and
+ * its gradients) record in one word per device, which is read and
+ * cleared here too.
  */
 int fk_device_error(fk_stream_t stream);
 
