@@ -23,6 +23,7 @@ Soft assignment (clustering_flashassign_b200.soft has the differentiable form):
 
     fk_logprob(x, c, ids, logp, lse, ...)       token log probabilities, entropy, top alternatives
     fk_logprob_backward(x, c, ids, lse, ...)    their gradients
+    fk_moe(x, router, w_in, w_out, y, ...)      mixture-of-experts layer for a few tokens
 """
 from __future__ import annotations
 
@@ -38,6 +39,7 @@ LIB_PATH = os.path.join(_HERE, "libfk.so")
 FK_F32, FK_F16, FK_BF16 = 0, 1, 2
 FK_OK, FK_EINVAL, FK_ENOMEM, FK_ECUDA, FK_ETIMEOUT, FK_EUNSUPPORTED = range(6)
 FK_HOST_AUTO, FK_HOST_RESIDENT, FK_HOST_STREAM = 0, 1, 2
+FK_ACT_SILU, FK_ACT_GELU = 0, 1
 FK_FAULT_NONE, FK_FAULT_ALLOC, FK_FAULT_H2D, FK_FAULT_LAUNCH = 0, 1, 2, 3
 
 DTYPES = {torch.float32: FK_F32, torch.float16: FK_F16, torch.bfloat16: FK_BF16}
@@ -47,7 +49,8 @@ EXPORTS = ["fk_assign", "fk_update", "fk_sort", "fk_lloyd", "fk_assign_noalloc",
            "fk_last_error", "fk_device_error", "fk_release", "fk_profile_enable", "fk_profile_read", "fk_profile_timeline",
            "fk_launch_count", "fk_version", "fk_selftest_bounded_wait", "fk_point_norms",
            "fk_init_centers", "fk_lloyd_step_partial", "fk_update_finalize", "fk_inject_fault",
-           "fk_logprob", "fk_logprob_workspace", "fk_logprob_backward", "fk_logprob_backward_workspace"]
+           "fk_logprob", "fk_logprob_workspace", "fk_logprob_backward", "fk_logprob_backward_workspace",
+           "fk_moe", "fk_moe_workspace"]
 
 
 class FkError(RuntimeError):
@@ -59,6 +62,10 @@ class FkError(RuntimeError):
 class FkShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_longlong), ("K", ctypes.c_int),
                 ("d", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class FkMoeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "E", "d", "F", "top_k", "dtype", "act", "renormalize")]
 
 
 class FkOptions(ctypes.Structure):
@@ -105,6 +112,8 @@ def _load():
         "fk_logprob": (I, [ctypes.POINTER(FkShape), P, P, P, F, P, P, P, P, I, P, P, P, LL, P]),
         "fk_logprob_workspace": (I, [ctypes.POINTER(FkShape), I, ctypes.POINTER(LL)]),
         "fk_logprob_backward": (I, [ctypes.POINTER(FkShape), P, P, P, F, P, P, P, P, P, P, P, P, P, P, LL, P]),
+        "fk_moe": (I, [ctypes.POINTER(FkMoeShape), P, P, P, P, P, P, P, P, LL, P]),
+        "fk_moe_workspace": (I, [ctypes.POINTER(FkMoeShape), ctypes.POINTER(LL)]),
         "fk_logprob_backward_workspace": (I, [ctypes.POINTER(FkShape), I, I, ctypes.POINTER(LL)]),
     }
     for name, (res, args) in sig.items():
@@ -355,6 +364,38 @@ def fk_logprob_backward(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, lse
         _check(lib.fk_logprob_backward(ctypes.byref(shape), _ptr(x), _ptr(c), _ptr(bias), float(scale), _ptr(ids),
                                        _ptr(lse), _ptr(entropy), _ptr(dlogp), _ptr(dlse), _ptr(dentropy), _ptr(dx),
                                        _ptr(dc), _ptr(dbias), _ptr(ws), ws.numel(), _stream(stream)), where)
+
+
+def fk_moe(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, y: torch.Tensor,
+           expert_ids: torch.Tensor, expert_weights: torch.Tensor, act: int = FK_ACT_SILU, renormalize: bool = True,
+           workspace=None, stream=None) -> torch.Tensor:
+    """y = sum over each token's best experts of w_j (act(x gate_j^T) * (x up_j^T)) w_out_j^T.
+
+    x (T,d), router (E,d), w_in (E,2F,d): gate rows then up rows, w_out (E,d,F), y (T,d), all fp16 or
+    all bf16; expert_ids / expert_weights (T,top_k) int32 / fp32, written.  workspace as in fk_logprob."""
+    where = "fk_moe"
+    if not x.is_cuda:
+        raise ValueError(f"{where}: x must be a CUDA tensor")
+    if x.dim() != 2 or router.dim() != 2 or w_out.dim() != 3 or expert_ids.dim() != 2:
+        raise ValueError(f"{where}: x must be (T, d), router (E, d), w_in (E, 2F, d), w_out (E, d, F), "
+                         "expert_ids (T, top_k)")
+    (T, d), E, F, k = x.shape, router.shape[0], w_out.shape[2], expert_ids.shape[1]
+    dev = x.device
+    _need(where, "router", router, x.dtype, (E, d), dev)
+    _need(where, "w_in", w_in, x.dtype, (E, 2 * F, d), dev)
+    _need(where, "w_out", w_out, x.dtype, (E, d, F), dev)
+    _need(where, "y", y, x.dtype, (T, d), dev)
+    _need(where, "expert_ids", expert_ids, torch.int32, (T, k), dev)
+    _need(where, "expert_weights", expert_weights, torch.float32, (T, k), dev)
+    shape = FkMoeShape(T, E, d, F, k, _dtype_code(x), int(act), int(bool(renormalize)))
+    with torch.cuda.device(dev):
+        need = ctypes.c_longlong(0)
+        _check(lib.fk_moe_workspace(ctypes.byref(shape), ctypes.byref(need)), where)
+        ws = workspace if workspace is not None else _scratch(need.value, dev, stream)
+        _need(where, "workspace", ws, torch.uint8, (ws.numel(),), dev)
+        _check(lib.fk_moe(ctypes.byref(shape), _ptr(x), _ptr(router), _ptr(w_in), _ptr(w_out), _ptr(y),
+                          _ptr(expert_ids), _ptr(expert_weights), _ptr(ws), ws.numel(), _stream(stream)), where)
+    return y
 
 
 def fk_device_error(stream=None) -> int:

@@ -1,13 +1,19 @@
-"""Soft assignment over libfk: token log probabilities and their gradients.
+"""Soft assignment over libfk: token log probabilities, and the experts they route to.
 
     r = token_log_probs(x, c, ids, top=5)
     r.logp, r.lse, r.entropy, r.top_ids, r.top_logp
+
+    m = expert_mixture(x, router, w_in, w_out, top_k=8)
+    m.y, m.expert_ids, m.expert_weights
 
 The soft form of the hard assignment: where fk_assign picks the nearest entry of a
 table for every row, this gives the log probability of a given entry (token, cluster)
 under the softmax of the row's scores, with the entropy of that distribution and its
 likeliest entries, without storing the scores.  It differentiates with respect to the
 rows, the table and the bias.
+
+expert_mixture sends each token to its likeliest entries of a small table (the router)
+and sums what these experts make of it: the serving form of a mixture-of-experts layer.
 """
 from __future__ import annotations
 
@@ -16,7 +22,7 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import fk_logprob, fk_logprob_backward
+from . import FK_ACT_GELU, FK_ACT_SILU, fk_logprob, fk_logprob_backward, fk_moe
 
 
 class TokenLogProbs(NamedTuple):
@@ -91,3 +97,39 @@ def token_log_probs(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, *, scal
     if c.dim() == 2:
         out = [None if t is None else t.reshape(lead + tuple(t.shape[2:])) for t in out]
     return TokenLogProbs(*out)
+
+
+class ExpertMixture(NamedTuple):
+    y: torch.Tensor
+    expert_ids: torch.Tensor       # int32, largest weight first
+    expert_weights: torch.Tensor   # fp32
+
+
+_ACTIVATIONS = {"silu": FK_ACT_SILU, "gelu": FK_ACT_GELU}
+
+
+def expert_mixture(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, top_k: int, *,
+                   renormalize: bool = True, activation: str = "silu") -> ExpertMixture:
+    """A mixture-of-experts layer for up to 256 tokens (forward only).
+
+    x (..., d) and router (E, d) score the experts; each token's top_k experts
+    (softmax over all, lowest index on ties; renormalize: their weights sum to
+    one) apply act(x gate^T) * (x up^T) with w_in (E, 2F, d), gate rows first,
+    and w_out (E, d, F).  fp16 or bf16 throughout; d and F multiples of 8.
+    It has no backward pass: with gradients enabled, inputs that require them
+    are refused.
+    """
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+    if torch.is_grad_enabled() and any(t.requires_grad for t in (x, router, w_in, w_out)):
+        raise RuntimeError("expert_mixture has no backward pass: call it under torch.no_grad()")
+    if x.dim() < 1:
+        raise ValueError("x must be (..., d)")
+    lead = tuple(x.shape[:-1])
+    xs = x.reshape(-1, x.shape[-1]).contiguous()
+    y = torch.empty_like(xs)
+    ids = torch.empty((xs.shape[0], int(top_k)), dtype=torch.int32, device=x.device)
+    weights = torch.empty((xs.shape[0], int(top_k)), dtype=torch.float32, device=x.device)
+    fk_moe(xs, router.contiguous(), w_in.contiguous(), w_out.contiguous(), y, ids, weights, _ACTIVATIONS[activation],
+           renormalize)
+    return ExpertMixture(y.reshape(x.shape), ids.reshape(lead + (int(top_k),)), weights.reshape(lead + (int(top_k),)))

@@ -360,6 +360,37 @@ int fk_logprob_backward(const fk_shape *shape, const void *x, const void *c, con
                         void *workspace, long long workspace_bytes, fk_stream_t stream);
 int fk_logprob_backward_workspace(const fk_shape *shape, int with_bias, int with_dbias, long long *bytes);
 
+/*
+ * fk_moe -- a mixture-of-experts layer for a few tokens, forward only (serving):
+ *     s = x router^T ; p = softmax(s) ; the top_k largest, lowest index on ties
+ *     w = p of the chosen, divided by their sum when renormalize != 0
+ *     h_j = act(x gate_j^T) * (x up_j^T) ;  y = sum_j w_j h_j w_out_j^T
+ * x (T, d), router (E, d), w_in (E, 2F, d): an expert's F gate rows, then its F
+ * up rows; w_out (E, d, F); y (T, d); expert_ids, expert_weights (T, top_k) int32
+ * / fp32, largest first.  fp16 or bf16 throughout (fp32: FK_EUNSUPPORTED), sums
+ * in fp32, scores in fp64.  Only the chosen experts' weights are read.
+ * Limits: 0 <= T <= 256, E <= 512, top_k <= min(E, 16), d and F multiples of 8.
+ * A NaN score ranks last; a token with one gets NaN weights and a NaN row of y
+ * and leaves the other tokens as they are.  Tensors 16-byte aligned (y, ids and
+ * weights by element).  Results do not depend on the order in which work is
+ * done.  Workspace as in fk_logprob, fk_moe_workspace bytes.
+ */
+typedef enum { FK_ACT_SILU = 0, FK_ACT_GELU = 1 /* erf form */ } fk_act;
+typedef struct {
+  int T;           /* tokens */
+  int E;           /* experts */
+  int d;           /* model width */
+  int F;           /* width of one expert */
+  int top_k;       /* experts per token */
+  int dtype;       /* FK_F16 or FK_BF16 */
+  int act;         /* fk_act */
+  int renormalize; /* weights of a token's experts sum to one */
+} fk_moe_shape;
+int fk_moe(const fk_moe_shape *shape, const void *x, const void *router, const void *w_in, const void *w_out,
+           void *y, int32_t *expert_ids, float *expert_weights, void *workspace, long long workspace_bytes,
+           fk_stream_t stream);
+int fk_moe_workspace(const fk_moe_shape *shape, long long *bytes);
+
 /* Static text for a status code. */
 const char *fk_status_string(int status);
 
@@ -371,8 +402,8 @@ const char *fk_last_error(void);
  * workspace.  Returns FK_OK, FK_ETIMEOUT (a bounded wait in a kernel gave
  * up), FK_EUNSUPPORTED (an fp16 squared norm of 2^32 or more reached the
  * tensor-core assign's norm digits) or FK_EINVAL (an id outside [0, K)
- * reached fk_update / fk_sort).  The soft assignment operators (fk_logprob and
- * its gradients) record in one word per device, which is read and
+ * reached fk_update / fk_sort).  The soft assignment operators (fk_logprob,
+ * its gradients and fk_moe) record in one word per device, which is read and
  * cleared here too.
  */
 int fk_device_error(fk_stream_t stream);
