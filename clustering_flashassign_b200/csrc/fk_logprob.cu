@@ -47,7 +47,7 @@ constexpr float kLowest = -256.f;
 // scores, and the final order is settled in fp64 among top + kSpare columns.
 constexpr int kSpare = 4;
 constexpr int kMaxTop = 28;  // top + kSpare candidates: one per lane of the joining warp
-constexpr int kCG = 1;
+constexpr int kCG = 2;
 
 __device__ __forceinline__ float ex2(float v) {
   float r;
@@ -785,7 +785,7 @@ int launch_tiles(const CUtensorMap &ta, const CUtensorMap &tb, Plan p, const typ
   constexpr uint32_t stage = tile::Geo<kCG>::kStageBytes;
   const size_t cap = 227 * 1024 - 1024 - tile::kCtrlBytes;
   p.stages = (int)std::min<size_t>(tile::kMaxStages, (cap - epi_smem) / stage);
-  p.stages = std::min(p.stages, 192 * 1024 / (int)stage);
+  
   p.idesc = sm100::idesc_f32acc((uint32_t)ab_fmt, tile::kRows * kCG, tile::kCols) | (A_MN ? 1u << 15 : 0u) |
             (B_MN ? 1u << 16 : 0u);
   const int smem = (int)(1024 + p.stages * stage + tile::kCtrlBytes + epi_smem);
