@@ -76,17 +76,17 @@ __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat
 // The 32 scores (base 2) of a thread's row in columns [col, col + 32) from the
 // accumulators.  A bias of -inf masks its column whatever the product holds.
 template <bool BIAS>
-__device__ __forceinline__ void scores32(const uint32_t (&r)[32], float scale2, const float *bias, long long col,
+__device__ __forceinline__ void scores32(const float (&r)[32], float scale2, const float *bias, long long col,
                                          long long K, float (&t)[32]) {
   if (BIAS) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       const float b = col + j < K ? __ldg(bias + col + j) : kNegInf;
-      t[j] = b == kNegInf ? kNegInf : fmaf(__uint_as_float(r[j]), scale2, b * kLog2e);
+      t[j] = b == kNegInf ? kNegInf : fmaf(r[j], scale2, b * kLog2e);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) t[j] = __uint_as_float(r[j]) * scale2;
+    for (int j = 0; j < 32; ++j) t[j] = r[j] * scale2;
     if (col + 32 > K) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
@@ -108,9 +108,18 @@ struct StatArgs {
   int32_t *top_i;
 };
 
-template <bool BIAS, bool TOP>
+// Running statistics of one row per thread.
+//
+// The best columns: a 32-column chunk whose maximum beats the row's list is
+// drained from its maximum downwards, every lane inserting its own best column
+// in the same step, until no lane's remainder beats its list.  The steps of a
+// chunk are then the most columns that any of the 32 rows keeps of it (after
+// the first few hundred columns mostly none), where a scan in column order
+// would pay one insertion for nearly every column that any row wants.
+template <bool BIAS, bool TOP, bool SEG>
 struct StatEpi {
   using Args = StatArgs;
+  static constexpr bool kSeg = SEG;
   static constexpr int kSlots = 32 * tile::kEpiWarps;
   const Args &a;
   const int r, half, slot;
@@ -119,6 +128,7 @@ struct StatEpi {
   const float *bias = nullptr;
   long long row = 0, at = 0;
   int id = -1;
+  bool idle = false;  // none of the warp's rows exists
   float m = 0.f, sum = 0.f, us = 0.f, tgt = 0.f, thr = 0.f;
 
   __device__ StatEpi(const Args &args, int lane, int r_in_tile, int half_, uint8_t *smem)
@@ -129,16 +139,19 @@ struct StatEpi {
 
   __device__ void begin(const Unit &w, long long row0) {
     row = row0 + r;
+    idle = row0 + (r & ~31) >= a.N;
     at = w.b * a.N + row;
     id = row < a.N ? __ldg(a.ids + at) : -1;
     if (BIAS) bias = a.bias + w.b * a.K;
     m = thr = tgt = kNegInf;
     sum = us = 0.f;
-    if (TOP)
+    if (TOP) {
       for (int j = 0; j < a.L; ++j) {
         lv[j * kSlots] = kNegInf;
         li[j * kSlots] = -1;
       }
+      if (row >= a.N) thr = INFINITY;  // a row beyond the last keeps nothing
+    }
   }
 
   __device__ __forceinline__ void insert(float v, int k) {
@@ -154,52 +167,57 @@ struct StatEpi {
     thr = lv[(a.L - 1) * kSlots];
   }
 
-  __device__ __forceinline__ void tile(uint32_t taddr, long long col0) {
-#pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-      const long long col = col0 + ch * 32;
-      if (col >= a.K) break;
-      uint32_t acc[32];
-      __syncwarp();  // the load is warp-wide; rows may have parted before it
-      sm100::tmem_ld_32x32b_x32(taddr + ch * 32, acc);
-      sm100::tmem_wait_ld();
-      float t[32];
-      scores32<BIAS>(acc, a.scale2, bias, col, a.K, t);
-      float cm = max3(t[0], t[1], t[2]);
+  static __device__ __forceinline__ float max32(const float (&t)[32]) {
+    float cm = max3(t[0], t[1], t[2]);
 #pragma unroll
-      for (int j = 3; j < 31; j += 2) cm = max3(cm, t[j], t[j + 1]);
-      cm = fmaxf(cm, t[31]);
-      if (cm > m) {
-        if (m != kNegInf) {
-          const float f = ex2(m - cm);
-          us = f * fmaf(m - cm, sum, us);
-          sum *= f;
-        }
-        m = cm;
+    for (int j = 3; j < 31; j += 2) cm = max3(cm, t[j], t[j + 1]);
+    return fmaxf(cm, t[31]);
+  }
+
+  __device__ __forceinline__ void chunk(const float (&acc)[32], long long col) {
+    float t[32];
+    scores32<BIAS>(acc, a.scale2, bias, col, a.K, t);
+    float cm = max32(t);
+    if (cm > m) {
+      if (m != kNegInf) {
+        const float f = ex2(m - cm);
+        us = f * fmaf(m - cm, sum, us);
+        sum *= f;
       }
-      const float ms = m == kNegInf ? 0.f : m;
-      float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
+      m = cm;
+    }
+    const float ms = m == kNegInf ? 0.f : m;
+    float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const float d0 = t[j] - ms, d1 = t[j + 1] - ms;
-        const float e0 = ex2(d0), e1 = ex2(d1);
-        s0 += e0;
-        s1 += e1;
-        u0 = fmaf(e0, fmaxf(d0, kLowest), u0);
-        u1 = fmaf(e1, fmaxf(d1, kLowest), u1);
-      }
-      sum += s0 + s1;
-      us += u0 + u1;
-      const unsigned rel = (unsigned)(id - (int)col);
-      if (__any_sync(0xffffffffu, rel < 32u)) {
+    for (int j = 0; j < 32; j += 2) {
+      const float d0 = t[j] - ms, d1 = t[j + 1] - ms;
+      const float e0 = ex2(d0), e1 = ex2(d1);
+      s0 += e0;
+      s1 += e1;
+      u0 = fmaf(e0, fmaxf(d0, kLowest), u0);
+      u1 = fmaf(e1, fmaxf(d1, kLowest), u1);
+    }
+    sum += s0 + s1;
+    us += u0 + u1;
+    const unsigned rel = (unsigned)(id - (int)col);
+    if (__any_sync(0xffffffffu, rel < 32u)) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (rel == (unsigned)j) tgt = t[j];
+    }
+    if (TOP) {
+      while (__any_sync(0xffffffffu, cm > thr)) {
+        const bool take = cm > thr;
+        int at_j = -1;
+#pragma unroll
+        for (int j = 31; j >= 0; --j)
+          if (t[j] == cm) at_j = j;
+        if (take) insert(cm, (int)col + at_j);
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (rel == (unsigned)j) tgt = t[j];
-      }
-      if (TOP && __any_sync(0xffffffffu, cm > thr)) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (t[j] > thr) insert(t[j], (int)col + j);
+          if (j == at_j) t[j] = kNegInf;
+        __syncwarp();
+        cm = max32(t);
       }
     }
   }
@@ -214,6 +232,7 @@ struct StatEpi {
         a.top_i[p * a.L + j] = li[j * kSlots];
       }
   }
+  __device__ __forceinline__ bool skip(long long col) const { return idle || col >= a.K; }
 };
 
 // Joins a row's partial results (one warp per row).
@@ -227,6 +246,7 @@ struct JoinArgs {
   float scale;
   long long rows, N, K;
   int d, parts, L, top;
+  bool vec;  // rows of x and c can be read 16 bytes at a time
   float *logp, *lse, *entropy, *top_logp;
   int32_t *top_ids;
   int *err;
@@ -244,39 +264,118 @@ __device__ __forceinline__ void join_stats(float &m, float &s, float &u, float m
   m = mm;
 }
 
-// Score of column k in fp64 by the whole warp, from the operands as given:
+// Scores of four columns in fp64, by LPR lanes, from the operands as given:
 // products of 16-bit values are exact, and fp64 sums keep neighbours in rank
 // apart that the fp32 accumulation cannot.
-template <typename T>
-__device__ double exact_score(const T *x, const T *c, const float *bias, float scale, int k, int d, int lane) {
-  const T *row = c + (size_t)k * d;
-  double s = 0.0;
-  for (int j = lane; j < d; j += 32) s += (double)to_f(x[j]) * (double)to_f(row[j]);
+template <typename T, int LPR>
+__device__ __forceinline__ void exact_scores(const T *x, const T *c, const float *bias, float scale, const int (&k)[4],
+                                             int d, bool vec, int lane, double (&s)[4]) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  s *= (double)scale;
-  if (bias) s = bias[k] == kNegInf ? (double)kNegInf : s + (double)bias[k];
-  return s;
+  for (int i = 0; i < 4; ++i) s[i] = 0.0;
+  constexpr int V = 16 / sizeof(T);
+  if (vec) {
+#pragma unroll 2
+    for (int j = lane; j < d / V; j += LPR) {
+      T xv[V], cv[4][V];
+      *reinterpret_cast<uint4 *>(xv) = __ldg(reinterpret_cast<const uint4 *>(x) + j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(cv[i]) = __ldg(reinterpret_cast<const uint4 *>(c + (size_t)k[i] * d) + j);
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const double xd = (double)to_f(xv[q]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = fma(xd, (double)to_f(cv[i][q]), s[i]);
+      }
+    }
+  } else {
+    for (int j = lane; j < d; j += LPR) {
+      const double xd = (double)to_f(x[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = fma(xd, (double)to_f(c[(size_t)k[i] * d + j]), s[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+    s[i] *= (double)scale;
+    if (bias) s[i] = bias[k[i]] == kNegInf ? (double)kNegInf : s[i] + (double)bias[k[i]];
+  }
 }
 
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
+constexpr int kNoCol = 0x7fffffff;
 
-template <typename T>
+// One warp's joined lists (and the row's candidates with their exact scores)
+// where eight warps share a row.
+struct JoinRow {
+  float m[kJoinWarps], s[kJoinWarps], u[kJoinWarps], tgt[kJoinWarps];
+  float v[kJoinWarps][32];
+  int k[kJoinWarps][32];
+  int cand[32];
+  double exact[32];
+};
+
+// The best L of the lanes' sorted lists (read through get(j, v, k)); lane j of
+// the group keeps the j-th.
+template <int LPR, class Get>
+__device__ __forceinline__ void draw(int L, int lane, Get get, float &mv, int &mk) {
+  int head = 0;
+  float hv;
+  int hk;
+  get(0, hv, hk);
+  mv = kNegInf;
+  mk = -1;
+  for (int j = 0; j < L; ++j) {
+    float v = hk >= 0 ? hv : kNegInf;
+    int k = hk >= 0 ? hk : kNoCol;
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) {
+      const float v2 = __shfl_xor_sync(0xffffffffu, v, o);
+      const int k2 = __shfl_xor_sync(0xffffffffu, k, o);
+      if (v2 > v || (v2 == v && k2 < k)) {
+        v = v2;
+        k = k2;
+      }
+    }
+    if (lane == j && k != kNoCol) {
+      mv = v;
+      mk = k;
+    }
+    if (hk == k) {
+      ++head;
+      hk = -1;
+      if (head < L) get(head, hv, hk);
+    }
+  }
+}
+
+// LPR lanes of WPR warps per row.  (8, 1): many rows of few parts, four rows a
+// warp; (32, 1); (32, 8): few rows, whose exact scores would otherwise be one
+// warp's long chain of loads.
+template <typename T, int LPR, int WPR>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
   extern __shared__ float join_smem[];
+  __shared__ JoinRow sh;
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long r = (long long)blockIdx.x * kJoinWarps + warp;
-  if (r >= a.rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & (LPR - 1);
+  const int sub = WPR > 1 ? warp : 0;  // this warp among the row's warps
+  const long long per_block = WPR > 1 ? 1 : kJoinWarps * (32 / LPR);
+  const long long r0 = (long long)blockIdx.x * per_block + (WPR > 1 ? 0 : threadIdx.x / LPR);
+  // lanes of a row beyond the last one follow along on the last row
+  const bool live = r0 < a.rows;
+  const long long r = live ? r0 : a.rows - 1;
   const long long b = r / a.N;
+  const int first = sub * LPR + lane, step = LPR * WPR;
   float m = kNegInf, s = 0.f, u = 0.f, tgt = kNegInf;
-  for (int p = lane; p < a.parts; p += 32) {
+  for (int p = first; p < a.parts; p += step) {
     const float4 q = a.part[r * a.parts + p];
     join_stats(m, s, u, q.x, q.y, q.z);
     tgt = fmaxf(tgt, q.w);
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
+  for (int o = LPR / 2; o; o >>= 1) {
     const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
     const float u2 = __shfl_xor_sync(0xffffffffu, u, o);
     // both sides join in the same order, so that all lanes hold the same bits
@@ -289,96 +388,147 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
     }
     tgt = fmaxf(tgt, __shfl_xor_sync(0xffffffffu, tgt, o));
   }
-  // log2 of the sum; a row whose columns are all masked has lse = -inf and an
-  // entropy of zero
+  if (WPR > 1) {
+    if (lane == 0) {
+      sh.m[warp] = m, sh.s[warp] = s, sh.u[warp] = u, sh.tgt[warp] = tgt;
+    }
+    __syncthreads();
+    m = sh.m[0], s = sh.s[0], u = sh.u[0], tgt = sh.tgt[0];
+    for (int w = 1; w < WPR; ++w) {
+      join_stats(m, s, u, sh.m[w], sh.s[w], sh.u[w]);
+      tgt = fmaxf(tgt, sh.tgt[w]);
+    }
+  }
+  // a row whose columns are all masked has lse = -inf and an entropy of zero
   const bool none = m == kNegInf && s == 0.f;
   const float ls = log2f(s);
-  const float lse2 = none ? kNegInf : m + ls;
-  const int id = a.ids[r];
-  const bool valid = id >= 0 && id < a.K;
-  if (lane == 0) {
+  if (live && lane == 0 && sub == 0) {
+    const int id = a.ids[r];
+    const bool valid = id >= 0 && id < a.K;
     if (id >= a.K) atomicCAS(a.err, DEV_OK, DEV_BAD_ID);
-    a.lse[r] = none ? kNegInf : lse2 * kLn2;
+    a.lse[r] = none ? kNegInf : (m + ls) * kLn2;
     if (a.entropy) a.entropy[r] = none ? 0.f : (ls - u / s) * kLn2;
     a.logp[r] = !valid ? 0.f : (none || (tgt == kNegInf && s == s)) ? kNegInf : ((tgt - m) - ls) * kLn2;
   }
   if (a.top == 0) return;
 
-  // each lane joins the sorted lists of its parts into one of its own ...
-  float *lv = join_smem + (size_t)warp * 64 * a.L + lane;
-  int32_t *li = reinterpret_cast<int32_t *>(join_smem + (size_t)warp * 64 * a.L + 32 * a.L) + lane;
-  for (int j = 0; j < a.L; ++j) {
-    lv[32 * j] = kNegInf;
-    li[32 * j] = -1;
-  }
-  for (int p = lane; p < a.parts; p += 32) {
-    const long long o = (r * a.parts + p) * a.L;
-    for (int j = 0; j < a.L; ++j) {
-      const float v = a.top_v[o + j];
-      const int k = a.top_i[o + j];
-      if (k < 0) break;
-      int q = a.L;
-      while (q > 0) {
-        const float w = lv[32 * (q - 1)];
-        const int wk = li[32 * (q - 1)];
-        if (wk >= 0 && (w > v || (w == v && wk < k))) break;
-        if (q < a.L) {
-          lv[32 * q] = w;
-          li[32 * q] = wk;
+  float mv;
+  int mine;
+  if (a.parts <= step) {  // one list per lane at most: drawn from where it lies
+    const long long o = (r * a.parts + first) * a.L;
+    draw<LPR>(a.L, lane,
+              [&](int j, float &v, int &k) {
+                k = -1;
+                if (first < a.parts) {
+                  v = __ldg(a.top_v + o + j);
+                  k = __ldg(a.top_i + o + j);
+                }
+              },
+              mv, mine);
+  } else {  // each lane joins the lists of its parts into one of its own first
+    float *lv = join_smem + (size_t)(threadIdx.x / LPR) * 2 * LPR * a.L + lane;
+    int32_t *li = reinterpret_cast<int32_t *>(join_smem + (size_t)(threadIdx.x / LPR) * 2 * LPR * a.L + LPR * a.L) + lane;
+    for (int j = 0; j < a.L; ++j) li[LPR * j] = -1;
+    for (int p = first; p < a.parts; p += step) {
+      const long long o = (r * a.parts + p) * a.L;
+      for (int j = 0; j < a.L; ++j) {
+        const float v = __ldg(a.top_v + o + j);
+        const int k = __ldg(a.top_i + o + j);
+        if (k < 0) break;
+        int q = a.L;
+        while (q > 0) {
+          const float w = lv[LPR * (q - 1)];
+          const int wk = li[LPR * (q - 1)];
+          if (wk >= 0 && (w > v || (w == v && wk < k))) break;
+          if (q < a.L) {
+            lv[LPR * q] = w;
+            li[LPR * q] = wk;
+          }
+          --q;
         }
-        --q;
-      }
-      if (q == a.L) break;
-      lv[32 * q] = v;
-      li[32 * q] = k;
-    }
-  }
-  __syncwarp();
-  // ... and the warp draws the best L heads; lane j keeps the j-th
-  int head = 0, mine = -1;
-  for (int j = 0; j < a.L; ++j) {
-    float v = head < a.L ? lv[32 * head] : kNegInf;
-    int k = head < a.L ? li[32 * head] : -1;
-    const int own = k;
-    if (k < 0) k = 0x7fffffff;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const float v2 = __shfl_xor_sync(0xffffffffu, v, o);
-      const int k2 = __shfl_xor_sync(0xffffffffu, k, o);
-      if (v2 > v || (v2 == v && k2 < k)) {
-        v = v2;
-        k = k2;
+        if (q == a.L) break;
+        lv[LPR * q] = v;
+        li[LPR * q] = k;
       }
     }
-    if (k == 0x7fffffff) break;  // every list is empty
-    if (own == k) ++head;
-    if (lane == j) mine = k;
+    __syncwarp();
+    draw<LPR>(a.L, lane,
+              [&](int j, float &v, int &k) {
+                v = lv[LPR * j];
+                k = li[LPR * j];
+              },
+              mv, mine);
   }
-  // masked (or NaN) columns are in no list: they follow, lowest index first
-  const unsigned found = __ballot_sync(0xffffffffu, mine >= 0);
-  if (__popc(found) < a.L) {
-    int next = 0;
-    for (int j = __popc(found); j < a.L; ++j, ++next) {
-      while (__any_sync(0xffffffffu, mine == next)) ++next;
-      if (lane == j) mine = next;
+  if (WPR > 1) {
+    sh.v[warp][lane] = mv;
+    sh.k[warp][lane] = mine;
+    __syncthreads();
+    if (warp == 0)
+      draw<LPR>(a.L, lane,
+                [&](int j, float &v, int &k) {
+                  k = -1;
+                  if (lane < WPR) {
+                    v = sh.v[lane][j];
+                    k = sh.k[lane][j];
+                  }
+                },
+                mv, mine);
+  }
+  const unsigned group = LPR == 32 ? 0u : (threadIdx.x & 31) & ~(LPR - 1u);  // first lane of the row's group
+  const unsigned mask = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << group;
+  if (sub == 0) {
+    // masked (or NaN) columns are in no list: they follow, lowest index first
+    const int found = __popc(__ballot_sync(0xffffffffu, mine >= 0) & mask);
+    if (__any_sync(0xffffffffu, found < a.L)) {
+      int next = 0;
+      for (int j = 0; j < a.L; ++j) {
+        const bool fill = j >= found;
+        for (;;) {
+          const bool listed = fill & ((__ballot_sync(0xffffffffu, mine == next) & mask) != 0u);
+          if (!__any_sync(0xffffffffu, listed)) break;
+          next += listed;
+        }
+        if (fill && lane == j) mine = next;
+        if (fill) ++next;
+      }
     }
+  }
+  if (WPR > 1) {
+    if (warp == 0) sh.cand[lane] = mine;
+    __syncthreads();
   }
   const T *x = static_cast<const T *>(a.x) + (size_t)r * a.d;
   const T *c = static_cast<const T *>(a.c) + (size_t)b * a.K * a.d;
   const float *bias = a.bias ? a.bias + b * a.K : nullptr;
   double v = (double)kNegInf;
-  for (int j = 0; j < a.L; ++j) {
-    const double e = exact_score<T>(x, c, bias, a.scale, __shfl_sync(0xffffffffu, mine, j), a.d, lane);
-    if (lane == j) v = e;
+  for (int j = 4 * sub; j < a.L; j += 4 * WPR) {
+    int k[4];
+    double e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int src = min(j + i, a.L - 1);
+      k[i] = WPR > 1 ? sh.cand[src] : __shfl_sync(0xffffffffu, mine, src, LPR);
+    }
+    exact_scores<T, LPR>(x, c, bias, a.scale, k, a.d, a.vec, lane, e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (lane == j + i) v = e[i];
+      if (WPR > 1 && lane == 0 && j + i < a.L) sh.exact[j + i] = e[i];
+    }
+  }
+  if (WPR > 1) {
+    __syncthreads();
+    if (warp != 0) return;
+    if (lane < a.L) v = sh.exact[lane];
   }
   const double rank_v = v == v ? v : (double)kNegInf;
   int rank = 0;
   for (int j = 0; j < a.L; ++j) {
-    const double v2 = __shfl_sync(0xffffffffu, rank_v, j);
-    const int k2 = __shfl_sync(0xffffffffu, mine, j);
+    const double v2 = __shfl_sync(0xffffffffu, rank_v, j, LPR);
+    const int k2 = __shfl_sync(0xffffffffu, mine, j, LPR);
     rank += v2 > rank_v || (v2 == rank_v && k2 < mine);
   }
-  if (lane < a.L && rank < a.top) {
+  if (live && lane < a.L && rank < a.top) {
     a.top_ids[r * a.top + rank] = mine;
     a.top_logp[r * a.top + rank] = v == (double)kNegInf && s == s ? kNegInf
                                                                   : (float)(v - (double)(none ? kNegInf : m) * M_LN2) -
@@ -444,9 +594,10 @@ struct GradArgs {
   long long nblk;
 };
 
-template <typename T, bool BIAS>
+template <typename T, bool BIAS, bool SEG>
 struct GradEpi {
   using Args = GradArgs;
+  static constexpr bool kSeg = SEG;
   const Args &a;
   const int r, lane;
   const float *bias = nullptr;
@@ -469,15 +620,9 @@ struct GradEpi {
     const long long blk = (row0 + (r & ~31)) >> 5;
     cp = a.colpart && blk < a.nblk ? a.colpart + (w.b * a.nblk + blk) * a.Kp : nullptr;
   }
-  __device__ __forceinline__ void tile(uint32_t taddr, long long col0) {
-#pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-      const long long col = col0 + ch * 32;
-      if (col >= a.Kp) break;
-      uint32_t acc[32];
-      __syncwarp();  // the load is warp-wide; rows may have parted before it
-      sm100::tmem_ld_32x32b_x32(taddr + ch * 32, acc);
-      sm100::tmem_wait_ld();
+  __device__ __forceinline__ bool skip(long long col) const { return col >= a.Kp; }
+  __device__ __forceinline__ void chunk(const float (&acc)[32], long long col) {
+    {
       float v[32];
       scores32<BIAS>(acc, a.scale2, bias, col, a.K, v);
       const int rel = q.id - (int)col;
@@ -562,9 +707,10 @@ __device__ __forceinline__ void store8(T *dst, const float (&v)[8], long long le
   }
 }
 
-template <typename T>
+template <typename T, bool SEG>
 struct StoreEpi {
   using Args = StoreArgs;
+  static constexpr bool kSeg = SEG;
   const Args &a;
   const int r;
   float alpha;
@@ -584,33 +730,25 @@ struct StoreEpi {
     out = static_cast<T *>(a.out) + w.b * a.batch_stride + row * a.pitch;
     if (a.part) part = a.part + w.ks * a.slot + (w.b * a.rows + row) * a.cols;
   }
-  __device__ __forceinline__ void tile(uint32_t taddr, long long col0) {
-#pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-      const long long col = col0 + ch * 32;
-      if (col >= a.cols) break;
-      uint32_t acc[32];
-      __syncwarp();  // the load is warp-wide; rows may have parted before it
-      sm100::tmem_ld_32x32b_x32(taddr + ch * 32, acc);
-      sm100::tmem_wait_ld();
-      if (row >= a.rows) continue;
+  __device__ __forceinline__ bool skip(long long col) const { return col >= a.cols; }
+  __device__ __forceinline__ void chunk(const float (&acc)[32], long long col) {
+    if (row >= a.rows) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long long left = a.cols - col - 8 * i;
-        float v[8];
+    for (int i = 0; i < 4; ++i) {
+      const long long left = a.cols - col - 8 * i;
+      float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(acc[8 * i + j]) * alpha;
-        if (!a.part) {
-          store8<T>(out + col + 8 * i, v, left, vec_t);
-        } else {
-          float *dst = part + col + 8 * i;
-          if (a.add) {
+      for (int j = 0; j < 8; ++j) v[j] = acc[8 * i + j] * alpha;
+      if (!a.part) {
+        store8<T>(out + col + 8 * i, v, left, vec_t);
+      } else {
+        float *dst = part + col + 8 * i;
+        if (a.add) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j < left) v[j] += dst[j];
-          }
-          store8<float>(dst, v, left, vec_f);
+          for (int j = 0; j < 8; ++j)
+            if (j < left) v[j] += dst[j];
         }
+        store8<float>(dst, v, left, vec_f);
       }
     }
   }
@@ -870,19 +1008,37 @@ int operand(const void *src, int dtype, long long rows, long long rows_per_b, in
   return launch_operand<__half>(src, rows, rows_per_b, d, dp, g, bias, dst, s);  // 16-bit rows are copied as bits
 }
 
+template <bool BIAS, bool SEG>
+int stats_seg(const CUtensorMap &tx, const CUtensorMap &tc, const FwdSpace &f, const StatArgs &a, int fmt, int *err,
+              cudaStream_t s) {
+  const size_t lists = (size_t)f.L * StatEpi<BIAS, true, SEG>::kSlots * 8;
+  if (f.L) return launch_tiles<StatEpi<BIAS, true, SEG>, false, false>(tx, tc, f.p, a, lists, fmt, err, s);
+  return launch_tiles<StatEpi<BIAS, false, SEG>, false, false>(tx, tc, f.p, a, 0, fmt, err, s);
+}
+
 template <bool BIAS>
 int scores_stats(const CUtensorMap &tx, const CUtensorMap &tc, const FwdSpace &f, const StatArgs &a, int fmt, int *err,
                  cudaStream_t s) {
-  const size_t lists = (size_t)f.L * StatEpi<BIAS, true>::kSlots * 8;
-  if (f.L) return launch_tiles<StatEpi<BIAS, true>, false, false>(tx, tc, f.p, a, lists, fmt, err, s);
-  return launch_tiles<StatEpi<BIAS, false>, false, false>(tx, tc, f.p, a, 0, fmt, err, s);
+  if (f.p.kblocks * f.p.pairs > tile::kSegBlocks) return stats_seg<BIAS, true>(tx, tc, f, a, fmt, err, s);
+  return stats_seg<BIAS, false>(tx, tc, f, a, fmt, err, s);
 }
 
+template <typename T, int LPR, int WPR>
+int launch_join_as(const JoinArgs &j, cudaStream_t s) {
+  const int per_block = WPR > 1 ? 1 : kJoinWarps * (32 / LPR);
+  const size_t smem = j.parts > LPR * WPR ? (size_t)kJoinWarps * 64 * j.L * 4 : 0;
+  if (smem) FK_TRY(set_smem_limit((const void *)k_join<T, LPR, WPR>, kJoinWarps * 64 * 32 * 4));
+  FK_CUDA(launch_pdl(k_join<T, LPR, WPR>, dim3((unsigned)cdiv(j.rows, per_block)), dim3(32 * kJoinWarps), smem, s, j));
+  return launched();
+}
+
+// Eight lanes hold eight candidates at most; a block per row pays while the
+// rows alone do not fill the SMs.
 template <typename T>
 int launch_join(const JoinArgs &j, cudaStream_t s) {
-  const size_t smem = (size_t)kJoinWarps * 64 * j.L * 4;
-  FK_CUDA(launch_pdl(k_join<T>, dim3((unsigned)cdiv(j.rows, kJoinWarps)), dim3(32 * kJoinWarps), smem, s, j));
-  return launched();
+  if (j.L && j.rows <= 4096) return launch_join_as<T, 32, 8>(j, s);
+  if (j.L <= 8 && j.parts <= 64) return launch_join_as<T, 8, 1>(j, s);
+  return launch_join_as<T, 32, 1>(j, s);
 }
 
 struct BwdSpace {
@@ -962,7 +1118,12 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
       ga.planes = m.planes;
       ga.colpart = dbias ? f.colpart : nullptr;
       ga.nblk = cdiv(nr, 32);
-      FK_TRY((launch_tiles<GradEpi<G, BIAS>, false, false>(tx, tc, pg, ga, 0, fmt, err, s)));
+      // scores as exact as the forward pass's where fp32 results hang on them;
+      // a 16-bit gradient does not show the difference (2^-15 against 2^-9)
+      if ((m.planes == 3 || dbias) && pg.kblocks * pg.pairs > tile::kSegBlocks)
+        FK_TRY((launch_tiles<GradEpi<G, BIAS, true>, false, false>(tx, tc, pg, ga, 0, fmt, err, s)));
+      else
+        FK_TRY((launch_tiles<GradEpi<G, BIAS, false>, false, false>(tx, tc, pg, ga, 0, fmt, err, s)));
       if (dbias) {
         FK_CUDA(launch_pdl(k_sum_cols, dim3((unsigned)cdiv(m.K, 32), bn), dim3(256), 0, s, (const float *)f.colpart,
                            ga.nblk, m.Kp, (long long)m.K, dbias + (size_t)b0 * m.K, r0 > 0 ? 1 : 0));
@@ -990,7 +1151,7 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
         sa.batch_stride = m.N * m.d;
         sa.part = px.ksplits > 1 ? f.partx : nullptr;
         sa.slot = (long long)bn * nr * m.d;
-        FK_TRY((launch_tiles<StoreEpi<T>, false, true>(tg, tcm, px, sa, 0, fmt, err, s)));
+        FK_TRY((launch_tiles<StoreEpi<T, sizeof(T) == 4>, false, true>(tg, tcm, px, sa, 0, fmt, err, s)));
         if (sa.part)
           FK_TRY(launch_sum_parts<T>(f.partx, px, bn, nr, m.d, sa.out, m.d, sa.batch_stride, s));
       }
@@ -1017,7 +1178,7 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
         sa.part = f.w_parts ? f.partw : nullptr;
         sa.slot = (long long)bn * m.K * m.d;
         sa.add = r0 > 0;
-        FK_TRY((launch_tiles<StoreEpi<T>, true, true>(tg, txm, pw, sa, 0, fmt, err, s)));
+        FK_TRY((launch_tiles<StoreEpi<T, sizeof(T) == 4>, true, true>(tg, txm, pw, sa, 0, fmt, err, s)));
         if (sa.part && r0 + nr >= m.N) {
           Plan all = f.pw;
           all.ksplits = f.nr < m.N ? f.pw.ksplits : pw.ksplits;
@@ -1116,6 +1277,7 @@ int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float 
   j.parts = a.parts, j.L = f.L, j.top = top;
   j.logp = logp, j.lse = lse, j.entropy = entropy, j.top_logp = top_logp, j.top_ids = top_ids;
   j.err = err;
+  j.vec = m.d * esize(m.dtype) % 16 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(c)) & 15) == 0;
   if (m.dtype == FK_F32) return launch_join<float>(j, s);
   if (m.dtype == FK_BF16) return launch_join<__nv_bfloat16>(j, s);
   return launch_join<__half>(j, s);

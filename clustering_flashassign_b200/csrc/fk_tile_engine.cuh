@@ -45,6 +45,11 @@ constexpr int kK = 64;       // contraction elements per stage
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr uint32_t kABytes = kRows * kK * 2;
+// A chain of tcgen05 accumulations rounds towards zero at every step, which adds
+// up to a bias of about steps / 2 half-units of the result (3e-6 of it at 2048
+// terms).  Epilogues that ask for it (kSeg) get the contraction in segments of
+// 512 terms, summed in registers with rounding to nearest.
+constexpr int kSegBlocks = 8;
 constexpr int kMaxStages = 8;
 constexpr int kCtrlBytes = 256;  // barriers, TMEM address, abort flag
 
@@ -203,11 +208,12 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // What an epilogue sees.  Epi provides
-//   struct Args                                 kernel argument
-//   static size_t smem_bytes                    (host side, own dynamic shared memory)
-//   begin(const Unit &)                         at the unit's first tile
-//   tile(tmem address of this warp's 32 rows and first column, column tile)
-//   end(const Unit &)                           after the unit's last tile
+//   struct Args                    kernel argument
+//   static constexpr bool kSeg     sum segments of the contraction in registers
+//   begin(const Unit &, row0)      before the unit's first tile
+//   skip(column)                   warp-uniform: nothing to do from this column on
+//   chunk(32 values, column)       the row's values of 32 consecutive columns
+//   end(const Unit &)              after the unit's last tile
 // and is constructed per thread with (args, lane, row in CTA tile, half, shared memory).
 template <int CG, bool A_MN, bool B_MN, class Epi>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -255,20 +261,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
+      int s = 0;
+      uint32_t ph = 1;  // parity of the stage's last release
       bool ok = true;
       for (int u = worker; u < p.units && ok; u += workers) {
         const Unit w = unit_of(p, u);
         const int arow = (w.rt * CG + (int)rank) * kRows;
         for (int ct = w.ct0; ct < w.ct1 && ok; ++ct) {
           const int bcol = ct * kCols + (int)rank * (kCols / CG);
+          int pair = w.k0 / p.kblocks, kb = w.k0 - pair * p.kblocks;
+          int pa, pb;
+          pair_planes(p.pairs, pair, pa, pb);
+          pa += w.b * p.planes;
+          pb += w.b * p.planes;
           for (int k = w.k0; k < w.k1; ++k, ++it) {
-            const int s = it % p.stages;
-            if (!mbar_wait_spin(empty(s), ((it / p.stages) & 1) ^ 1, abort_flag, err)) { ok = false; break; }
-            const int pair = k / p.kblocks, kb = k - pair * p.kblocks;
-            int pa, pb;
-            pair_planes(p.pairs, pair, pa, pb);
-            pa += w.b * p.planes;
-            pb += w.b * p.planes;
+            if (!mbar_wait_spin(empty(s), ph, abort_flag, err)) { ok = false; break; }
             const uint32_t sa = base + s * G::kStageBytes, sb = sa + kABytes;
             const uint32_t bar = CG == 1 ? full(s) : map_to_cta(full(s), 0);
             if (rank == 0) mbar_arrive_expect_tx(full(s), G::kStageBytes * CG);
@@ -285,6 +292,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_3d<CG>(&tb, sb + i * 8192u, bar, bcol + i * 64, kb * kK, pb);
             } else {
               load_3d<CG>(&tb, sb, bar, kb * kK, bcol, pb);
+            }
+            if (++kb == p.kblocks) {
+              kb = 0;
+              if (++pair < p.pairs) {
+                pair_planes(p.pairs, pair, pa, pb);
+                pa += w.b * p.planes;
+                pb += w.b * p.planes;
+              }
+            }
+            if (++s == p.stages) {
+              s = 0;
+              ph ^= 1;
             }
           }
         }
@@ -303,29 +322,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      uint32_t it = 0, n = 0;
+      uint32_t n = 0;
+      int s = 0;
+      uint32_t ph = 0;
       bool ok = true;
       for (int u = worker; u < p.units && ok; u += workers) {
         const Unit w = unit_of(p, u);
-        for (int ct = w.ct0; ct < w.ct1 && ok; ++ct, ++n) {
-          const uint32_t buf = n & 1;
-          if (!mbar_wait_spin(tempty(buf), ((n >> 1) & 1) ^ 1, abort_flag, err)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t d = tmem + buf * kCols;
-          for (int k = w.k0; k < w.k1; ++k, ++it) {
-            const int s = it % p.stages;
-            if (!mbar_wait_spin(full(s), (it / p.stages) & 1, abort_flag, err)) { ok = false; break; }
+        for (int ct = w.ct0; ct < w.ct1 && ok; ++ct) {
+          for (int ks = w.k0; ks < w.k1 && ok; ++n) {
+            const int ke = Epi::kSeg && w.k1 - ks > kSegBlocks ? ks + kSegBlocks : w.k1;
+            const uint32_t buf = n & 1;
+            if (!mbar_wait_spin(tempty(buf), ((n >> 1) & 1) ^ 1, abort_flag, err)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t sa = base + s * G::kStageBytes, sb = sa + kABytes;
+            const uint32_t d = tmem + buf * kCols;
+            for (int k = ks; k < ke; ++k) {
+              if (!mbar_wait_spin(full(s), ph, abort_flag, err)) { ok = false; break; }
+              tc_fence_after();
+              const uint32_t sa = base + s * G::kStageBytes, sb = sa + kABytes;
 #pragma unroll
-            for (int kk = 0; kk < kK / 16; ++kk) {
-              const uint64_t da = A_MN ? desc_mn_sw128(sa + kk * 2048u) : desc_k_sw128(sa + kk * 32u);
-              const uint64_t db = B_MN ? desc_mn_sw128(sb + kk * 2048u) : desc_k_sw128(sb + kk * 32u);
-              mma<CG>(d, da, db, p.idesc, k > w.k0 || kk > 0);
+              for (int kk = 0; kk < kK / 16; ++kk) {
+                const uint64_t da = A_MN ? desc_mn_sw128(sa + kk * 2048u) : desc_k_sw128(sa + kk * 32u);
+                const uint64_t db = B_MN ? desc_mn_sw128(sb + kk * 2048u) : desc_k_sw128(sb + kk * 32u);
+                mma<CG>(d, da, db, p.idesc, k > ks || kk > 0);
+              }
+              commit<CG>(empty(s));
+              if (++s == p.stages) {
+                s = 0;
+                ph ^= 1;
+              }
             }
-            commit<CG>(empty(s));
+            if (ok) commit<CG>(tfull(buf));
+            ks = ke;
           }
-          if (ok) commit<CG>(tfull(buf));
         }
       }
     }
@@ -334,20 +362,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     Epi epi(ea, lane, quad * 32 + lane, half, ctrl_gen + kCtrlBytes);
     uint32_t n = 0;
     bool ok = true;
+    auto release = [&](uint32_t buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 1 || rank == 0) mbar_arrive(tempty(buf));
+        else arrive_cluster(map_to_cta(tempty(buf), 0));
+      }
+    };
     for (int u = worker; u < p.units && ok; u += workers) {
       const Unit w = unit_of(p, u);
       epi.begin(w, (w.rt * CG + (int)rank) * kRows);
-      for (int ct = w.ct0; ct < w.ct1; ++ct, ++n) {
-        const uint32_t buf = n & 1;
-        if (!warp_wait(tfull(buf), (n >> 1) & 1, abort_flag, err, lane)) { ok = false; break; }
-        tc_fence_after();
-        epi.tile(tmem + buf * kCols + half * (kCols / 2) + ((uint32_t)(quad * 32) << 16),
-                 (long long)ct * kCols + half * (kCols / 2));
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 1 || rank == 0) mbar_arrive(tempty(buf));
-          else arrive_cluster(map_to_cta(tempty(buf), 0));
+      for (int ct = w.ct0; ct < w.ct1 && ok; ++ct) {
+        const long long col0 = (long long)ct * kCols + half * (kCols / 2);
+        const uint32_t lanes = tmem + half * (kCols / 2) + ((uint32_t)(quad * 32) << 16);
+        if constexpr (Epi::kSeg) {
+          float sum[4][32];
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[ch][j] = 0.f;
+          for (int ks = w.k0; ks < w.k1 && ok; ks += kSegBlocks, ++n) {
+            const uint32_t buf = n & 1;
+            if (!warp_wait(tfull(buf), (n >> 1) & 1, abort_flag, err, lane)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t acc[32];
+              if (!epi.skip(col0 + ch * 32)) {
+                tmem_ld_32x32b_x32(lanes + buf * kCols + ch * 32, acc);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[ch][j] += __uint_as_float(acc[j]);
+              }
+            }
+            release(buf);
+          }
+          if (ok) {
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+              if (!epi.skip(col0 + ch * 32)) {
+                epi.chunk(sum[ch], col0 + ch * 32);
+                __syncwarp();
+              }
+          }
+        } else {
+          const uint32_t buf = n & 1;
+          if (!warp_wait(tfull(buf), (n >> 1) & 1, abort_flag, err, lane)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            if (epi.skip(col0 + ch * 32)) break;
+            float acc[32];
+            tmem_ld_32x32b_x32(lanes + buf * kCols + ch * 32, reinterpret_cast<uint32_t(&)[32]>(acc));
+            tmem_wait_ld();
+            epi.chunk(acc, col0 + ch * 32);
+            __syncwarp();  // the next load is warp-wide
+          }
+          release(buf);
+          ++n;
         }
       }
       if (ok) epi.end(w);
