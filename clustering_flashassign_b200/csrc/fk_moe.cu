@@ -10,29 +10,33 @@
 // (3 F d values each) once from HBM; every expert is read for all its tokens
 // together, as the sort-inverse update gathers the points of one cluster.
 //
-// k_route: one cluster of 8 CTAs per 8 tokens.  The CTAs share the experts;
-// scores are summed in fp64 (products of 16-bit values are exact, so experts
-// are ranked by their exact scores) and sent to the CTA of their token, which
-// draws the k best.
+// k_route: one cluster of 8 CTAs per 8 tokens.  The CTAs share the experts; a
+// thread keeps its slice of the 8 tokens in registers and meets every expert's
+// row with it.  Scores are summed in fp64 (products of 16-bit values are exact,
+// so experts are ranked by their exact scores) and sent to the CTA of their
+// token, which ranks the experts by counting the better ones.
 //
 // k_experts: a persistent kernel over units of weights, taken from a ticket
 // counter in the order  gate/up of expert 0, 1, ..., down of expert 0, 1, ...
 //   gate/up unit   8 gate rows and the 8 up rows of the same columns: the 16
 //                  rows of one mma.sync m16n8k16, whose 8 columns are tokens,
 //   down unit      16 rows of Wd against the expert's h.
-// The 8 warps of a CTA split a unit's contraction, so that a unit is one round
-// of loads deep, and join through shared memory.  A lane loads 16 consecutive
-// bytes of a row; the contraction's order inside a 32-element step is free, so
-// these 8 elements feed two MMA steps without a transpose.  (tcgen05 has
-// nothing to offer here: 128 rows of weights would meet 8 token columns, and
-// the weights would take a detour through shared memory; the register path
-// streams them at the rate HBM gives.)
+// A unit belongs to a group of 1, 2, 4 or 8 warps that split its contraction:
+// as few as still give every warp of the GPU something to do.  One warp per
+// unit needs no barrier and no joining and streams on its own; with few units
+// (one token) the split keeps enough loads in flight.
+// A lane loads 16 consecutive bytes of a row; the contraction's order inside a
+// 32-element step is free, so these 8 elements feed two MMA steps without a
+// transpose.  (tcgen05 has nothing to offer here: 128 rows of weights would
+// meet 8 token columns, and the weights would take a detour through shared
+// memory; the register path streams them at the rate HBM gives.)
 // A down unit waits until its expert's h is complete.  Tickets make that safe
 // without a grid-wide barrier or a cooperative launch: whoever waits holds a
-// later ticket than every unit it waits for, and those are held by CTAs that
-// run already.  Products of the k experts are written per (token, slot) and
-// the CTA that finishes a block of 16 output columns sums its slots in order,
-// so results do not depend on the order of arrival.
+// later ticket than every unit it waits for, and those are held by warps that
+// run already and do not wait themselves.  Products of the k experts are
+// written per (token, slot) and the group that finishes a block of 16 output
+// columns sums its slots in order, so results do not depend on the order of
+// arrival.
 //
 // h is held as hi + lo of the weights' type (bf16: 16 significant bits; fp16:
 // 22, of h / 64 to keep the type's range ahead of h), so that rounding it does
@@ -87,115 +91,140 @@ struct Two<__nv_bfloat16> {
 };
 
 // ------------------------------------------------------------------ routing
+constexpr int kPerCta = kMaxExperts / kRouteCtas;  // experts of one CTA at most
+
+// Order of a score as an integer; NaN ranks with -inf, below everything else.
+__device__ __forceinline__ unsigned long long score_key(double v) {
+  if (!(v == v)) return 0ull;
+  const long long b = __double_as_longlong(v == 0.0 ? 0.0 : v);
+  const unsigned long long k = b < 0 ? ~(unsigned long long)b : (unsigned long long)b | (1ull << 63);
+  return v == -INFINITY ? 0ull : k;
+}
+
 template <typename T>
 __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(32 * kWarps) k_route(const MoeArgs a) {
+  __shared__ double part[kWarps][kPerCta][kRouteCtas];
   __shared__ double scores[kMaxExperts];
+  __shared__ unsigned long long keys[kMaxExperts];
+  __shared__ int sel[kMaxTopK];
   cg::cluster_group cluster = cg::this_cluster();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = (int)cluster.block_rank();
   const int t0 = (blockIdx.x / kRouteCtas) * kRouteCtas;
   const int nt = min(kRouteCtas, a.T - t0);
   pdl_wait();
   pdl_trigger();
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.counters; i += gridDim.x * blockDim.x) a.tickets[i] = 0;
-  const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + (size_t)t0 * a.d);
-  const int n = a.d / 8;
-  cluster.sync();  // every CTA of the cluster runs before its memory is written
-  for (int e = cta * kWarps + warp; e < a.E; e += kRouteCtas * kWarps) {
-    const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.router) + (size_t)e * a.d);
-    double acc[kRouteCtas] = {};
-    for (int i = lane; i < n; i += 32) {
-      const uint4 rv = __ldg(r + i);
-      const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
-      double rd[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = Two<T>::f(rw[j]);
-        rd[2 * j] = f.x;
-        rd[2 * j + 1] = f.y;
-      }
-#pragma unroll
-      for (int t = 0; t < kRouteCtas; ++t) {
-        if (t < nt) {
-          const uint4 xv = __ldg(x + (size_t)t * n + i);
-          const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = Two<T>::f(xw[j]);
-            acc[t] = fma((double)f.x, rd[2 * j], acc[t]);
-            acc[t] = fma((double)f.y, rd[2 * j + 1], acc[t]);
-          }
-        }
-      }
-    }
+  for (int i = blockIdx.x * blockDim.x + tid; i < a.counters; i += gridDim.x * blockDim.x) a.tickets[i] = 0;
+  const T *xs = static_cast<const T *>(a.x) + (size_t)t0 * a.d;
+  const T *rs = static_cast<const T *>(a.router);
+  const int mine = a.E > cta ? (a.E - cta + kRouteCtas - 1) / kRouteCtas : 0;  // experts cta, cta + 8, ...
+  for (int k0 = 0; k0 < a.d; k0 += 8 * 32 * kWarps) {
+    const int k = k0 + tid * 8;
+    double x[kRouteCtas][8];
 #pragma unroll
     for (int t = 0; t < kRouteCtas; ++t) {
       if (t < nt) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (k < a.d) v = __ldg(reinterpret_cast<const uint4 *>(xs + (size_t)t * a.d + k));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int o = 16; o; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-        if (lane == 0) *cluster.map_shared_rank(scores + e, t) = acc[t];
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = Two<T>::f(w[j]);
+          x[t][2 * j] = f.x;
+          x[t][2 * j + 1] = f.y;
+        }
       }
+    }
+    for (int e0 = 0; e0 < mine; e0 += 4) {
+      uint4 r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[i] = make_uint4(0, 0, 0, 0);
+        if (e0 + i < mine && k < a.d)
+          r[i] = __ldg(reinterpret_cast<const uint4 *>(rs + (size_t)(cta + (e0 + i) * kRouteCtas) * a.d + k));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (e0 + i >= mine) break;
+        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+        double rd[8], acc[kRouteCtas];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = Two<T>::f(w[j]);
+          rd[2 * j] = f.x;
+          rd[2 * j + 1] = f.y;
+        }
+#pragma unroll
+        for (int t = 0; t < kRouteCtas; ++t) {
+          acc[t] = 0.0;
+          if (t < nt) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[t] = fma(x[t][j], rd[j], acc[t]);
+          }
+        }
+        double *out = part[warp][e0 + i];
+        if (nt == 1) {
+#pragma unroll
+          for (int o = 16; o; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+          if (lane == 0) out[0] = k0 ? out[0] + acc[0] : acc[0];
+        } else {
+          // eight sums over 32 lanes: three exchanges halve the tokens a lane
+          // carries, two more add up the four copies; lanes 0, 4, ... hold one each
+#pragma unroll
+          for (int o = 4; o; o >>= 1) {
+            const bool up = lane & (o * 4);
+#pragma unroll
+            for (int t = 0; t < o; ++t) {
+              const double keep = up ? acc[t + o] : acc[t], give = up ? acc[t] : acc[t + o];
+              acc[t] = keep + __shfl_xor_sync(0xffffffffu, give, o * 4);
+            }
+          }
+          acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
+          acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 2);
+          if ((lane & 3) == 0) out[lane >> 2] = k0 ? out[lane >> 2] + acc[0] : acc[0];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  cluster.sync();  // every CTA of the cluster runs before its memory is written
+  for (int i = tid; i < mine * kRouteCtas; i += blockDim.x) {
+    const int e = i / kRouteCtas, t = i % kRouteCtas;
+    if (t < nt) {
+      double v = 0.0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += part[w][e][t];
+      *cluster.map_shared_rank(scores + cta + e * kRouteCtas, t) = v;
     }
   }
   cluster.sync();
-  if (warp != 0 || cta >= nt) return;
-  const int t = t0 + cta;
-  constexpr int kPer = kMaxExperts / 32;
-  const double none = -INFINITY;
-  double v[kPer];
-  double big = none;
-  bool nan = false;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int e = lane + 32 * j;
-    v[j] = e < a.E ? scores[e] : none;
-    nan |= !(v[j] == v[j]);
-    if (v[j] > big) big = v[j];
+  if (cta >= nt) return;
+  for (int e = tid; e < a.E; e += blockDim.x) keys[e] = score_key(scores[e]);
+  __syncthreads();
+  for (int e = tid; e < a.E; e += blockDim.x) {
+    const unsigned long long key = keys[e];
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < a.E; ++i) rank += keys[i] > key || (keys[i] == key && i < e);
+    if (rank < a.k) sel[rank] = e;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) big = fmax(big, __shfl_xor_sync(0xffffffffu, big, o));
-  nan = __any_sync(0xffffffffu, nan);
-  float all = 0.f;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (lane + 32 * j < a.E) all += expf((float)(v[j] - big));
+  __syncthreads();
+  if (warp != 0) return;
+  const double big = scores[sel[0]];
+  const float p = lane < a.k ? expf((float)(scores[sel[lane]] - big)) : 0.f;
+  float all = p;
+  bool nan = false;
+  if (!a.renorm) all = 0.f;
+  for (int e = lane; e < a.E; e += 32) {
+    nan |= !(scores[e] == scores[e]);
+    if (!a.renorm) all += expf((float)(scores[e] - big));
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  uint32_t taken = 0;
-  int my_e = 0;
-  float my_p = 0.f, chosen = 0.f;
-  for (int j = 0; j < a.k; ++j) {
-    // the best expert left; NaN and -inf scores rank last, lowest index first
-    double bv = none;
-    int be = 0x7fffffff;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 32 * i;
-      if (e < a.E && !(taken >> i & 1u) && (be == 0x7fffffff || v[i] > bv)) {
-        be = e;
-        bv = v[i] > none ? v[i] : none;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const double v2 = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int e2 = __shfl_xor_sync(0xffffffffu, be, o);
-      if (v2 > bv || (v2 == bv && e2 < be)) {
-        bv = v2;
-        be = e2;
-      }
-    }
-    if ((be & 31) == lane) taken |= 1u << (be >> 5);
-    const float p = nan ? NAN : expf((float)(bv - big));
-    chosen += p;
-    if (lane == j) {
-      my_e = be;
-      my_p = p;
-    }
-  }
+  nan = __any_sync(0xffffffffu, nan);
   if (lane < a.k) {
-    a.ids[t * a.k + lane] = my_e;
-    a.weights[t * a.k + lane] = my_p / (a.renorm ? chosen : all);
+    a.ids[(t0 + cta) * a.k + lane] = sel[lane];
+    a.weights[(t0 + cta) * a.k + lane] = nan ? NAN : p / all;
   }
 }
 
@@ -234,26 +263,27 @@ __device__ __forceinline__ int load_acquire(const int *p) {
   return v;
 }
 
-// c[n] += rows (lo row, hi row of this lane) x tokens over this warp's share of
-// `steps` 32-element steps.  SPLIT: the tokens' side is hi + lo.
+// c[n] += rows (lo row, hi row of this lane) x tokens over the 32-element
+// steps sub, sub + S, ... of a group of S warps.  SPLIT: the tokens' side is hi + lo.
 template <typename T, int NT, bool SPLIT>
 __device__ __forceinline__ void contract(float (&c)[NT][4], const T *r0, const T *r1, const T *const (&tok)[NT],
-                                         const T *const (&tok2)[NT], int len, int warp, int q) {
-  constexpr int U = NT == 1 ? 4 : 2;  // steps in flight
+                                         const T *const (&tok2)[NT], int len, int sub, int S, int q) {
+  constexpr int U = NT == 1 ? (SPLIT ? 4 : 6) : NT == 2 ? 3 : 2;  // steps in flight
   constexpr bool BF = Two<T>::kBf;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k0 = warp * 32; k0 < len; k0 += 32 * kWarps * U) {
+  const int step = 32 * S;
+  for (int k0 = sub * 32 + q * 8; k0 < len + q * 8; k0 += step * U) {
     uint4 A0[U], A1[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * 32 * kWarps + q * 8;
+      const int k = k0 + u * step;
       A0[u] = r0 && k < len ? stream16(r0 + k) : zero;
       A1[u] = r1 && k < len ? stream16(r1 + k) : zero;
     }
     uint4 B[U][NT], B2[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * 32 * kWarps + q * 8;
+      const int k = k0 + u * step;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const bool in = tok[n] && k < len;
@@ -283,19 +313,43 @@ __device__ __forceinline__ void contract(float (&c)[NT][4], const T *r0, const T
 constexpr int kMaxNT = 4;  // tokens of one pass over a unit's weights: 32
 
 struct ExpertSmem {
-  float red[kWarps][kMaxNT][16][8];
+  float red[kWarps][kMaxNT][4][32];    // a warp's accumulators, where warps share a unit
   int first[kMaxExperts + 1];          // an expert's entries in `slots`
   int fill[kMaxExperts];
   int active[kMaxExperts];
   unsigned short slots[kMaxTokens * kMaxTopK];  // token * k + choice, by expert
-  int n_active, ticket, last, ok;
+  int n_active;
+  int word[kWarps];                    // a group's ticket or verdict, handed to its warps
 };
 
+// A group of S consecutive warps of the CTA.
+struct Group {
+  int S, id, sub, lane;
+  __device__ __forceinline__ bool leader() const { return sub == 0 && lane == 0; }
+  __device__ __forceinline__ void sync() const {
+    if (S == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(S * 32) : "memory");
+  }
+  // every thread of the group gets the leader's value
+  __device__ __forceinline__ int share(ExpertSmem &sm, int v) const {
+    if (S == 1) return __shfl_sync(0xffffffffu, v, 0);
+    if (leader()) sm.word[id] = v;
+    sync();
+    const int r = *(volatile int *)&sm.word[id];
+    sync();
+    return r;
+  }
+};
+
+__device__ __forceinline__ float activate(int act, float g) {
+  return act == FK_ACT_SILU ? g / (1.f + expf(-g)) : 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+}
+
 template <typename T, int NT, bool DOWN>
-__device__ __forceinline__ void unit_pass(const MoeArgs &a, ExpertSmem &sm, int e, int base, int count, int row0,
-                                          int lane, int warp) {
+__device__ __forceinline__ void unit_pass(const MoeArgs &a, ExpertSmem &sm, const Group &gr, int e, int base, int count,
+                                          int row0) {
   constexpr bool BF = Two<T>::kBf;
-  const int g = lane >> 2, q = lane & 3;
+  const int g = gr.lane >> 2, q = gr.lane & 3;
   const T *r0, *r1;
   const int len = DOWN ? a.F : a.d;
   if (DOWN) {
@@ -322,56 +376,83 @@ __device__ __forceinline__ void unit_pass(const MoeArgs &a, ExpertSmem &sm, int 
     }
   }
   float c[NT][4] = {};
-  contract<T, NT, DOWN>(c, r0, r1, tok, tok2, len, warp, q);
+  contract<T, NT, DOWN>(c, r0, r1, tok, tok2, len, gr.sub, gr.S, q);
+  if (gr.S > 1) {  // the group's first warps take one tile of 8 tokens each and add up its parts
+    const int w0 = gr.id * gr.S;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sm.red[w0 + gr.sub][n][i][gr.lane] = c[n][i];
+    gr.sync();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (n % gr.S != gr.sub) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v = 0.f;
+        for (int w = 0; w < gr.S; ++w) v += sm.red[w0 + w][n][i][gr.lane];
+        c[n][i] = v;
+      }
+    }
+  }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    *reinterpret_cast<float2 *>(&sm.red[warp][n][g][2 * q]) = make_float2(c[n][0], c[n][1]);
-    *reinterpret_cast<float2 *>(&sm.red[warp][n][g + 8][2 * q]) = make_float2(c[n][2], c[n][3]);
-  }
-  __syncthreads();
-  if (DOWN) {
-    for (int i = threadIdx.x; i < NT * 128; i += 32 * kWarps) {
-      const int n = i >> 7, col = (i >> 4) & 7, row = i & 15;
-      if (n * 8 + col < count && row0 + row < a.d) {
-        float v = 0.f;
+    if (gr.S > 1 && n % gr.S != gr.sub) continue;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += sm.red[w][n][row][col];
-        const int slot = sm.slots[base + n * 8 + col];
-        a.part[(size_t)slot * a.d + row0 + row] = v * (a.weights[slot] * (BF ? 1.f : 1.f / kHalfScale));
-      }
-    }
-  } else {
-    for (int i = threadIdx.x; i < NT * 64; i += 32 * kWarps) {
-      const int n = i >> 6, col = (i >> 3) & 7, row = i & 7;
-      if (n * 8 + col < count) {
-        float gate = 0.f, up = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          gate += sm.red[w][n][row][col];
-          up += sm.red[w][n][row + 8][col];
+    for (int i = 0; i < 2; ++i) {
+      // this lane: rows g (c[n][i]) and g + 8 (c[n][2 + i]) of token 2 q + i
+      const int col = n * 8 + 2 * q + i;
+      if (col < count) {
+        const int slot = sm.slots[base + col];
+        if (DOWN) {
+          const float w = a.weights[slot] * (BF ? 1.f : 1.f / kHalfScale);
+          float *out = a.part + (size_t)slot * a.d + row0 + g;
+          if (row0 + g < a.d) out[0] = c[n][i] * w;
+          if (row0 + 8 + g < a.d) out[8] = c[n][2 + i] * w;
+        } else {
+          float h = activate(a.act, c[n][i]) * c[n][2 + i];
+          if (!BF) h *= kHalfScale;
+          const size_t at = (size_t)slot * a.F + row0 + g;
+          const T hi = static_cast<T>(h);
+          static_cast<T *>(a.hi)[at] = hi;
+          static_cast<T *>(a.lo)[at] = static_cast<T>(h - static_cast<float>(hi));
         }
-        const float act = a.act == FK_ACT_SILU ? gate / (1.f + expf(-gate))
-                                               : 0.5f * gate * (1.f + erff(gate * 0.70710678118654752f));
-        float h = act * up;
-        if (!BF) h *= kHalfScale;
-        const size_t at = (size_t)sm.slots[base + n * 8 + col] * a.F + row0 + row;
-        const T hi = static_cast<T>(h);
-        static_cast<T *>(a.hi)[at] = hi;
-        static_cast<T *>(a.lo)[at] = static_cast<T>(h - static_cast<float>(hi));
       }
     }
   }
-  __syncthreads();
+  gr.sync();
 }
 
 template <typename T, bool DOWN>
-__device__ __forceinline__ void unit(const MoeArgs &a, ExpertSmem &sm, int e, int row0, int lane, int warp) {
+__device__ __forceinline__ void unit(const MoeArgs &a, ExpertSmem &sm, const Group &gr, int e, int row0) {
   const int end = sm.first[e + 1];
   for (int base = sm.first[e]; base < end; base += 8 * kMaxNT) {
     const int count = min(end - base, 8 * kMaxNT);
-    if (count <= 8) unit_pass<T, 1, DOWN>(a, sm, e, base, count, row0, lane, warp);
-    else if (count <= 16) unit_pass<T, 2, DOWN>(a, sm, e, base, count, row0, lane, warp);
-    else unit_pass<T, 4, DOWN>(a, sm, e, base, count, row0, lane, warp);
+    if (count <= 8) unit_pass<T, 1, DOWN>(a, sm, gr, e, base, count, row0);
+    else if (count <= 16) unit_pass<T, 2, DOWN>(a, sm, gr, e, base, count, row0);
+    else unit_pass<T, 4, DOWN>(a, sm, gr, e, base, count, row0);
+  }
+}
+
+// Columns [blk * 16, + 16) of y: the slots of each token, in order.  A lane
+// takes four columns (d is a multiple of 8).
+template <typename T>
+__device__ __forceinline__ void sum_slots(const MoeArgs &a, const Group &gr, int blk) {
+  const int who = gr.sub * 32 + gr.lane, col = blk * 16 + (who & 3) * 4;
+  if (col >= a.d) return;
+  for (int t = who >> 2; t < a.T; t += 8 * gr.S) {
+    const float *p = a.part + (size_t)t * a.k * a.d + col;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int j = 0; j < a.k; ++j) {
+      const float4 w = __ldcg(reinterpret_cast<const float4 *>(p + (size_t)j * a.d));
+      v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    }
+    T *y = static_cast<T *>(a.y) + (size_t)t * a.d + col;
+    y[0] = static_cast<T>(v.x);
+    y[1] = static_cast<T>(v.y);
+    y[2] = static_cast<T>(v.z);
+    y[3] = static_cast<T>(v.w);
   }
 }
 
@@ -410,64 +491,51 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_experts(const MoeArgs a) {
   }
   __syncthreads();
   for (int i = tid; i < slots; i += blockDim.x) sm.slots[atomicAdd(&sm.fill[a.ids[i]], 1)] = (unsigned short)i;
-  if (tid == 0) sm.ticket = atomicAdd(a.tickets, 1);
   __syncthreads();
 
   const int ups = a.F / 8, downs = (a.d + 15) / 16;
   const int n_up = sm.n_active * ups, n_all = n_up + sm.n_active * downs;
   int *done_up = a.tickets + 1, *done_block = a.tickets + 1 + a.E;
-  for (;;) {
-    const int t = sm.ticket;
-    __syncthreads();
-    if (t >= n_all) return;
+  // the fewest warps per unit that give every warp of the grid one
+  const int warps = (int)gridDim.x * kWarps, units = min(n_up, n_all - n_up);
+  int S = 1;
+  while (S < kWarps && (long long)units * S < warps) S *= 2;
+  const Group gr = {S, warp / S, warp % S, lane};
+  int t = gr.share(sm, gr.leader() ? atomicAdd(a.tickets, 1) : 0);
+  while (t < n_all) {
     int next = 0;
-    if (tid == 0) next = atomicAdd(a.tickets, 1);  // in flight under this unit's loads
+    if (gr.leader()) next = atomicAdd(a.tickets, 1);  // in flight under this unit's loads
     if (t < n_up) {
       const int ae = t / ups, e = sm.active[ae];
-      unit<T, false>(a, sm, e, (t - ae * ups) * 8, lane, warp);
-      if (tid == 0) {
+      unit<T, false>(a, sm, gr, e, (t - ae * ups) * 8);
+      if (gr.leader()) {
         __threadfence();
         atomicAdd(done_up + e, 1);
       }
     } else {
       const int ae = (t - n_up) / downs, blk = (t - n_up) - ae * downs, e = sm.active[ae];
-      if (tid == 0) {
-        int ok = 1;
-        if (load_acquire(done_up + e) < ups) {
-          const unsigned long long t0 = sm100::globaltimer();
-          while (load_acquire(done_up + e) < ups) {
-            if (sm100::globaltimer() - t0 > kWaitLimitNs) {
-              atomicCAS(a.err, DEV_OK, DEV_TIMEOUT);
-              ok = 0;
-              break;
-            }
-          }
-        }
-        sm.ok = ok;
-      }
-      __syncthreads();
-      if (!sm.ok) return;
-      unit<T, true>(a, sm, e, blk * 16, lane, warp);
-      if (tid == 0) {
-        __threadfence();
-        sm.last = atomicAdd(done_block + blk, 1) == sm.n_active - 1;
-      }
-      __syncthreads();
-      if (sm.last) {
-        __threadfence();
-        // the block's 16 columns of y: the slots of each token, in order
-        for (int i = tid; i < a.T * 16; i += blockDim.x) {
-          const int tok = i >> 4, col = blk * 16 + (i & 15);
-          if (col < a.d) {
-            float v = 0.f;
-            for (int j = 0; j < a.k; ++j) v += __ldcg(a.part + (size_t)(tok * a.k + j) * a.d + col);
-            static_cast<T *>(a.y)[(size_t)tok * a.d + col] = static_cast<T>(v);
+      int ok = 1;
+      if (gr.leader() && load_acquire(done_up + e) < ups) {
+        const unsigned long long t0 = sm100::globaltimer();
+        while (load_acquire(done_up + e) < ups) {
+          if (sm100::globaltimer() - t0 > kWaitLimitNs) {
+            atomicCAS(a.err, DEV_OK, DEV_TIMEOUT);
+            ok = 0;
+            break;
           }
         }
       }
+      if (!gr.share(sm, ok)) return;
+      unit<T, true>(a, sm, gr, e, blk * 16);
+      int last = 0;
+      if (gr.leader()) {
+        __threadfence();
+        last = atomicAdd(done_block + blk, 1) == sm.n_active - 1;
+        __threadfence();
+      }
+      if (gr.share(sm, last)) sum_slots<T>(a, gr, blk);
     }
-    if (tid == 0) sm.ticket = next;
-    __syncthreads();
+    t = gr.share(sm, next);
   }
 }
 
