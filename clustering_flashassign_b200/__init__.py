@@ -277,26 +277,49 @@ def fk_update_finalize(sums: torch.Tensor, counts: torch.Tensor, centers: torch.
     return centers
 
 
-def _need(where: str, name: str, t, dtype, shape, device) -> None:
-    """A CUDA tensor of this dtype, shape and device; None passes."""
+def _need(where: str, name: str, t, dtype, shape, device) -> int | None:
+    """Address of a contiguous CUDA tensor of this dtype, shape and device; None for None."""
     if t is None:
-        return
-    if t.device != device:
-        raise ValueError(f"{where}: {name} is on {t.device}, not on {device}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{where}: {name} must be {dtype} of shape {tuple(shape)}, "
-                         f"got {t.dtype} of shape {tuple(t.shape)}")
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{where}: {name} must be {dtype} of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} of shape {tuple(t.shape)} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """Caller-owned workspace: torch's allocator ties it to the stream the call runs on
-    (a captured graph keeps its own)."""
+_here = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream without its object
+
+
+def _at(device):
+    """Context in which `device` is current (free where it is already)."""
+    return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _handle(stream, device) -> int:
+    """cudaStream_t of the stream a call runs on (None: torch's current one on `device`)."""
     if stream is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _scratch(where: str, workspace, nbytes: int, device, stream):
+    """(workspace, address, bytes): the caller's, or a new one that torch's allocator ties to
+    the stream the call runs on (a captured graph keeps its own)."""
+    if workspace is None:
+        if stream is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif workspace.dtype != torch.uint8 or workspace.dim() != 1:
+        raise ValueError(f"{where}: workspace must be a one-dimensional uint8 tensor")
+    n = workspace.numel()
+    return workspace, _need(where, "workspace", workspace, torch.uint8, (n,), device), n
 
 
 def _soft_shape(where, x, c):
@@ -305,9 +328,7 @@ def _soft_shape(where, x, c):
     if x.dim() != 3 or c.dim() != 3:
         raise ValueError(f"{where}: x must be (B, N, d) and c (B, K, d)")
     (B, N, d), K = x.shape, c.shape[1]
-    code = _dtype_code(x)
-    _need(where, "c", c, x.dtype, (B, K, d), x.device)
-    return FkShape(B, N, K, d, code), B, N, K
+    return FkShape(B, N, K, d, _dtype_code(x)), B, N, K, d
 
 
 def fk_logprob(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, logp: torch.Tensor, lse: torch.Tensor,
@@ -318,25 +339,26 @@ def fk_logprob(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, logp: torch.
     x (B,N,d), c (B,K,d), ids (B,N) int32, bias (B,K) fp32; logp / lse / entropy (B,N) fp32,
     top_ids / top_logp (B,N,top) int32 / fp32.  workspace: a uint8 tensor of at least
     fk_logprob_workspace bytes (None: allocated here)."""
-    where = "fk_logprob"
-    shape, B, N, K = _soft_shape(where, x, c)
-    dev, f32 = x.device, torch.float32
-    for name, t in (("ids", ids), ("logp", logp), ("lse", lse), ("entropy", entropy)):
-        _need(where, name, t, torch.int32 if name == "ids" else f32, (B, N), dev)
-    _need(where, "bias", bias, f32, (B, K), dev)
+    w = "fk_logprob"
+    shape, B, N, K, d = _soft_shape(w, x, c)
+    dev, f32, i32, row = x.device, torch.float32, torch.int32, (B, N)
     if (top_ids is None) != (top_logp is None):
-        raise ValueError(f"{where}: top_ids and top_logp come together")
+        raise ValueError(f"{w}: top_ids and top_logp come together")
     top = 0 if top_ids is None else top_ids.shape[-1]
-    _need(where, "top_ids", top_ids, torch.int32, (B, N, top), dev)
-    _need(where, "top_logp", top_logp, f32, (B, N, top), dev)
-    with torch.cuda.device(dev):
+    px, pc = _need(w, "x", x, x.dtype, (B, N, d), dev), _need(w, "c", c, x.dtype, (B, K, d), dev)
+    pb, pi = _need(w, "bias", bias, f32, (B, K), dev), _need(w, "ids", ids, i32, row, dev)
+    pl, ps = _need(w, "logp", logp, f32, row, dev), _need(w, "lse", lse, f32, row, dev)
+    pe = _need(w, "entropy", entropy, f32, row, dev)
+    pti = _need(w, "top_ids", top_ids, i32, (B, N, top), dev)
+    ptl = _need(w, "top_logp", top_logp, f32, (B, N, top), dev)
+    with _at(dev):
         need = ctypes.c_longlong(0)
-        _check(lib.fk_logprob_workspace(ctypes.byref(shape), top, ctypes.byref(need)), where)
-        ws = workspace if workspace is not None else _scratch(need.value, dev, stream)
-        _need(where, "workspace", ws, torch.uint8, (ws.numel(),), dev)
-        _check(lib.fk_logprob(ctypes.byref(shape), _ptr(x), _ptr(c), _ptr(bias), float(scale), _ptr(ids), _ptr(logp),
-                              _ptr(lse), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logp), _ptr(ws), ws.numel(),
-                              _stream(stream)), where)
+        if st := lib.fk_logprob_workspace(ctypes.byref(shape), top, ctypes.byref(need)):
+            _check(st, w)
+        workspace, pw, n = _scratch(w, workspace, need.value, dev, stream)
+        if st := lib.fk_logprob(ctypes.byref(shape), px, pc, pb, scale, pi, pl, ps, pe, top, pti, ptl, pw, n,
+                                _handle(stream, dev)):
+            _check(st, w)
     return logp
 
 
@@ -345,25 +367,25 @@ def fk_logprob_backward(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, lse
                         scale: float = 1.0, workspace=None, stream=None) -> None:
     """Gradients of fk_logprob into dx (B,N,d), dc (B,K,d) (x's dtype) and dbias (B,K) fp32, each optional,
     from upstream gradients dlogp, dlse, dentropy (B,N) fp32, each optional."""
-    where = "fk_logprob_backward"
-    shape, B, N, K = _soft_shape(where, x, c)
-    dev, f32 = x.device, torch.float32
-    for name, t in (("ids", ids), ("lse", lse), ("entropy", entropy), ("dlogp", dlogp), ("dlse", dlse),
-                    ("dentropy", dentropy)):
-        _need(where, name, t, torch.int32 if name == "ids" else f32, (B, N), dev)
-    _need(where, "dx", dx, x.dtype, x.shape, dev)
-    _need(where, "dc", dc, x.dtype, c.shape, dev)
-    _need(where, "bias", bias, f32, (B, K), dev)
-    _need(where, "dbias", dbias, f32, (B, K), dev)
-    with torch.cuda.device(dev):
+    w = "fk_logprob_backward"
+    shape, B, N, K, d = _soft_shape(w, x, c)
+    dev, f32, row, dt = x.device, torch.float32, (B, N), x.dtype
+    px, pc = _need(w, "x", x, dt, (B, N, d), dev), _need(w, "c", c, dt, (B, K, d), dev)
+    pb, pi = _need(w, "bias", bias, f32, (B, K), dev), _need(w, "ids", ids, torch.int32, row, dev)
+    ps, pe = _need(w, "lse", lse, f32, row, dev), _need(w, "entropy", entropy, f32, row, dev)
+    ga, gl = _need(w, "dlogp", dlogp, f32, row, dev), _need(w, "dlse", dlse, f32, row, dev)
+    ge = _need(w, "dentropy", dentropy, f32, row, dev)
+    pdx, pdc = _need(w, "dx", dx, dt, (B, N, d), dev), _need(w, "dc", dc, dt, (B, K, d), dev)
+    pdb = _need(w, "dbias", dbias, f32, (B, K), dev)
+    with _at(dev):
         need = ctypes.c_longlong(0)
-        _check(lib.fk_logprob_backward_workspace(ctypes.byref(shape), int(bias is not None), int(dbias is not None),
-                                                 ctypes.byref(need)), where)
-        ws = workspace if workspace is not None else _scratch(need.value, dev, stream)
-        _need(where, "workspace", ws, torch.uint8, (ws.numel(),), dev)
-        _check(lib.fk_logprob_backward(ctypes.byref(shape), _ptr(x), _ptr(c), _ptr(bias), float(scale), _ptr(ids),
-                                       _ptr(lse), _ptr(entropy), _ptr(dlogp), _ptr(dlse), _ptr(dentropy), _ptr(dx),
-                                       _ptr(dc), _ptr(dbias), _ptr(ws), ws.numel(), _stream(stream)), where)
+        if st := lib.fk_logprob_backward_workspace(ctypes.byref(shape), bias is not None, dbias is not None,
+                                                   ctypes.byref(need)):
+            _check(st, w)
+        workspace, pw, n = _scratch(w, workspace, need.value, dev, stream)
+        if st := lib.fk_logprob_backward(ctypes.byref(shape), px, pc, pb, scale, pi, ps, pe, ga, gl, ge, pdx, pdc, pdb,
+                                         pw, n, _handle(stream, dev)):
+            _check(st, w)
 
 
 def fk_moe(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, y: torch.Tensor,
@@ -373,28 +395,26 @@ def fk_moe(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_out: tor
 
     x (T,d), router (E,d), w_in (E,2F,d): gate rows then up rows, w_out (E,d,F), y (T,d), all fp16 or
     all bf16; expert_ids / expert_weights (T,top_k) int32 / fp32, written.  workspace as in fk_logprob."""
-    where = "fk_moe"
+    w = "fk_moe"
     if not x.is_cuda:
-        raise ValueError(f"{where}: x must be a CUDA tensor")
+        raise ValueError(f"{w}: x must be a CUDA tensor")
     if x.dim() != 2 or router.dim() != 2 or w_out.dim() != 3 or expert_ids.dim() != 2:
-        raise ValueError(f"{where}: x must be (T, d), router (E, d), w_in (E, 2F, d), w_out (E, d, F), "
+        raise ValueError(f"{w}: x must be (T, d), router (E, d), w_in (E, 2F, d), w_out (E, d, F), "
                          "expert_ids (T, top_k)")
     (T, d), E, F, k = x.shape, router.shape[0], w_out.shape[2], expert_ids.shape[1]
-    dev = x.device
-    _need(where, "router", router, x.dtype, (E, d), dev)
-    _need(where, "w_in", w_in, x.dtype, (E, 2 * F, d), dev)
-    _need(where, "w_out", w_out, x.dtype, (E, d, F), dev)
-    _need(where, "y", y, x.dtype, (T, d), dev)
-    _need(where, "expert_ids", expert_ids, torch.int32, (T, k), dev)
-    _need(where, "expert_weights", expert_weights, torch.float32, (T, k), dev)
-    shape = FkMoeShape(T, E, d, F, k, _dtype_code(x), int(act), int(bool(renormalize)))
-    with torch.cuda.device(dev):
+    dev, dt = x.device, x.dtype
+    px, pr = _need(w, "x", x, dt, (T, d), dev), _need(w, "router", router, dt, (E, d), dev)
+    pin, pout = _need(w, "w_in", w_in, dt, (E, 2 * F, d), dev), _need(w, "w_out", w_out, dt, (E, d, F), dev)
+    py, pi = _need(w, "y", y, dt, (T, d), dev), _need(w, "expert_ids", expert_ids, torch.int32, (T, k), dev)
+    pg = _need(w, "expert_weights", expert_weights, torch.float32, (T, k), dev)
+    shape = FkMoeShape(T, E, d, F, k, _dtype_code(x), act, bool(renormalize))
+    with _at(dev):
         need = ctypes.c_longlong(0)
-        _check(lib.fk_moe_workspace(ctypes.byref(shape), ctypes.byref(need)), where)
-        ws = workspace if workspace is not None else _scratch(need.value, dev, stream)
-        _need(where, "workspace", ws, torch.uint8, (ws.numel(),), dev)
-        _check(lib.fk_moe(ctypes.byref(shape), _ptr(x), _ptr(router), _ptr(w_in), _ptr(w_out), _ptr(y),
-                          _ptr(expert_ids), _ptr(expert_weights), _ptr(ws), ws.numel(), _stream(stream)), where)
+        if st := lib.fk_moe_workspace(ctypes.byref(shape), ctypes.byref(need)):
+            _check(st, w)
+        workspace, pw, n = _scratch(w, workspace, need.value, dev, stream)
+        if st := lib.fk_moe(ctypes.byref(shape), px, pr, pin, pout, py, pi, pg, pw, n, _handle(stream, dev)):
+            _check(st, w)
     return y
 
 

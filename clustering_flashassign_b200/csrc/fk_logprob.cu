@@ -47,7 +47,10 @@ constexpr float kLowest = -256.f;
 // scores, and the final order is settled in fp64 among top + kSpare columns.
 constexpr int kSpare = 4;
 constexpr int kMaxTop = 28;  // top + kSpare candidates: one per lane of the joining warp
-constexpr int kCG = 2;
+// One CTA's 128 rows hold all rows: the second half of a pair's 256-row tile
+// would be empty, and single CTAs spread a short run of columns over all SMs.
+// Otherwise pairs.
+inline int group_of(long long rows) { return rows <= tile::kRows ? 1 : 2; }
 
 __device__ __forceinline__ float ex2(float v) {
   float r;
@@ -862,8 +865,9 @@ long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 // the start and the partial results of a unit counted as a quarter of a tile.
 Plan plan_runs(int B, long long rows, long long cols, int kdim, int pairs, int planes, int row_bytes) {
   Plan p = {};
-  const int workers = num_sms() / kCG;
-  p.row_tiles = (int)cdiv(rows, tile::kRows * kCG);
+  p.cg = group_of(rows);
+  const int workers = num_sms() / p.cg;
+  p.row_tiles = (int)cdiv(rows, tile::kRows * p.cg);
   p.col_tiles = (int)cdiv(cols, tile::kCols);
   p.kblocks = (int)cdiv(kdim, tile::kK);
   p.pairs = pairs;
@@ -879,7 +883,7 @@ Plan plan_runs(int B, long long rows, long long cols, int kdim, int pairs, int p
     }
   }
   // rows of one group: 32 MB of the row operand at most, so that they stay in L2
-  const long long g = (32LL << 20) / ((long long)tile::kRows * kCG * row_bytes);
+  const long long g = (32LL << 20) / ((long long)tile::kRows * p.cg * row_bytes);
   p.group = (int)std::max(1LL, std::min<long long>(g, p.row_tiles));
   p.units = (int)((long long)B * p.row_tiles * p.runs);
   return p;
@@ -889,8 +893,9 @@ Plan plan_runs(int B, long long rows, long long cols, int kdim, int pairs, int p
 // mostly idle; a split costs about eight K-blocks (its partial sums).
 Plan plan_splits(int B, long long rows, long long cols, long long kdim, int pairs, int planes) {
   Plan p = {};
-  const int workers = num_sms() / kCG;
-  p.row_tiles = (int)cdiv(rows, tile::kRows * kCG);
+  p.cg = group_of(rows);
+  const int workers = num_sms() / p.cg;
+  p.row_tiles = (int)cdiv(rows, tile::kRows * p.cg);
   p.col_tiles = (int)cdiv(cols, tile::kCols);
   p.runs = p.col_tiles;
   p.kblocks = (int)cdiv(kdim, tile::kK);
@@ -907,7 +912,7 @@ Plan plan_splits(int B, long long rows, long long cols, long long kdim, int pair
       p.ksplits = ks;
     }
   }
-  p.group = std::max(1, std::min(p.row_tiles, 16 / kCG));
+  p.group = std::max(1, std::min(p.row_tiles, 16 / p.cg));
   p.units = (int)((long long)B * p.row_tiles * p.runs * p.ksplits);
   return p;
 }
@@ -916,8 +921,8 @@ bool too_many(const Plan &p, int B) {
   return (double)B * p.row_tiles * p.runs * p.ksplits > 2e9;
 }
 
-template <class Epi, bool A_MN, bool B_MN>
-int launch_tiles(const CUtensorMap &ta, const CUtensorMap &tb, Plan p, const typename Epi::Args &ea, size_t epi_smem,
+template <int kCG, class Epi, bool A_MN, bool B_MN>
+int launch_group(const CUtensorMap &ta, const CUtensorMap &tb, Plan p, const typename Epi::Args &ea, size_t epi_smem,
                  int ab_fmt, int *err, cudaStream_t s) {
   auto kern = tile::k_tiles<kCG, A_MN, B_MN, Epi>;
   constexpr uint32_t stage = tile::Geo<kCG>::kStageBytes;
@@ -945,6 +950,13 @@ int launch_tiles(const CUtensorMap &ta, const CUtensorMap &tb, Plan p, const typ
   cfg.numAttrs = kCG > 1 ? 2 : 1;
   FK_CUDA(cudaLaunchKernelEx(&cfg, kern, ta, tb, p, ea, err));
   return launched();
+}
+
+template <class Epi, bool A_MN, bool B_MN>
+int launch_tiles(const CUtensorMap &ta, const CUtensorMap &tb, const Plan &p, const typename Epi::Args &ea,
+                 size_t epi_smem, int ab_fmt, int *err, cudaStream_t s) {
+  if (p.cg == 1) return launch_group<1, Epi, A_MN, B_MN>(ta, tb, p, ea, epi_smem, ab_fmt, err, s);
+  return launch_group<2, Epi, A_MN, B_MN>(ta, tb, p, ea, epi_smem, ab_fmt, err, s);
 }
 
 // Tensor map of 16-bit elements: (inner, rows, depth) with the row pitch and
@@ -1101,13 +1113,13 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
       const long long nr = std::min(f.nr, m.N - r0);
       const size_t xoff = ((size_t)b0 * m.planes * m.N + r0) * m.dp * 2, coff = (size_t)b0 * m.planes * m.K * m.dp * 2;
       // scores again, and from them G
+      Plan pg = f.pg;
+      if (bn != f.bn || nr != f.nr) pg = plan_runs(bn, nr, m.Kp, m.d, m.pairs, m.planes, m.dp * 2 * m.planes);
       CUtensorMap tx, tc;
       FK_TRY(map_16(&tx, (const char *)xo + xoff, bf, m.dp, nr, (long long)bn * m.planes, m.dp, m.N * m.dp, tile::kK,
                     tile::kRows));
       FK_TRY(map_16(&tc, (const char *)co + coff, bf, m.dp, m.K, (long long)bn * m.planes, m.dp, (long long)m.K * m.dp,
-                    tile::kK, tile::kCols / kCG));
-      Plan pg = f.pg;
-      if (bn != f.bn || nr != f.nr) pg = plan_runs(bn, nr, m.Kp, m.d, m.pairs, m.planes, m.dp * 2 * m.planes);
+                    tile::kK, tile::kCols / pg.cg));
       GradArgs ga = {};
       ga.scale2 = scale * kLog2e;
       ga.bias = bias ? bias + (size_t)b0 * m.K : nullptr;
@@ -1259,7 +1271,7 @@ int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float 
   CUtensorMap tx, tc;
   FK_TRY(map_16(&tx, xo, bf, m.dp, m.N, (long long)m.B * m.planes, m.dp, m.N * m.dp, tile::kK, tile::kRows));
   FK_TRY(map_16(&tc, co, bf, m.dp, m.K, (long long)m.B * m.planes, m.dp, (long long)m.K * m.dp, tile::kK,
-                tile::kCols / kCG));
+                tile::kCols / f.p.cg));
   StatArgs a = {};
   a.scale2 = scale * kLog2e;
   a.bias = bias;

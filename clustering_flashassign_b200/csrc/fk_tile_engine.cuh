@@ -60,6 +60,7 @@ struct Geo {
 };
 
 struct Plan {
+  int cg;           // CTAs per tile
   int units;        // B * ksplits * runs * row_tiles
   int row_tiles;    // tiles of 128 * CG rows
   int col_tiles;

@@ -33,35 +33,48 @@ class TokenLogProbs(NamedTuple):
     top_logp: Optional[torch.Tensor]
 
 
+def _forward(x, c, bias, ids, scale, top):
+    rows, dev = ids.shape, x.device
+    logp, lse, entropy = (torch.empty(rows, dtype=torch.float32, device=dev) for _ in range(3))
+    top_ids = top_logp = None
+    if top:
+        top_ids = torch.empty((*rows, top), dtype=torch.int32, device=dev)
+        top_logp = torch.empty((*rows, top), dtype=torch.float32, device=dev)
+    fk_logprob(x, c, ids, logp, lse, entropy, top_ids, top_logp, bias, scale)
+    return logp, lse, entropy, top_ids, top_logp
+
+
+def _backward(ctx, dlogp, dlse, dentropy, *_):
+    x, c, bias, ids, lse, entropy = ctx.saved_tensors
+    if dlogp is None and dlse is None and dentropy is None:
+        return (None,) * 6
+    up = [None if g is None else g.contiguous() for g in (dlogp, dlse, dentropy)]
+    want = ctx.needs_input_grad
+    dx = torch.empty_like(x) if want[0] else None
+    dc = torch.empty_like(c) if want[1] else None
+    dbias = torch.empty_like(bias) if want[2] else None
+    fk_logprob_backward(x, c, ids, lse, entropy, *up, dx, dc, dbias, bias, ctx.scale)
+    return dx, dc, dbias, None, None, None
+
+
+_backward_once = once_differentiable(_backward)
+
+
 class _LogProbs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, c, bias, ids, scale, top):
-        B, N, _ = x.shape
-        row = dict(dtype=torch.float32, device=x.device)
-        logp, lse, entropy = torch.empty(3, B, N, **row).unbind(0)
-        top_ids = torch.empty((B, N, top), dtype=torch.int32, device=x.device) if top else None
-        top_logp = torch.empty((B, N, top), **row) if top else None
-        fk_logprob(x, c, ids, logp, lse, entropy, top_ids, top_logp, bias, scale)
-        ctx.save_for_backward(x, c, bias, ids, lse, entropy)
+        out = _forward(x, c, bias, ids, scale, top)
+        ctx.save_for_backward(x, c, bias, ids, out[1], out[2])
         ctx.scale = scale
         ctx.set_materialize_grads(False)
         if top:
-            ctx.mark_non_differentiable(top_ids, top_logp)
-        return logp, lse, entropy, top_ids, top_logp
+            ctx.mark_non_differentiable(*out[3:])
+        return out
 
     @staticmethod
-    @once_differentiable
-    def backward(ctx, dlogp, dlse, dentropy, *_):
-        x, c, bias, ids, lse, entropy = ctx.saved_tensors
-        up = [None if g is None else g.float().contiguous() for g in (dlogp, dlse, dentropy)]
-        if all(g is None for g in up):
-            return (None,) * 6
-        want = ctx.needs_input_grad
-        dx = torch.empty_like(x) if want[0] else None
-        dc = torch.empty_like(c) if want[1] else None
-        dbias = torch.empty_like(bias) if want[2] else None
-        fk_logprob_backward(x, c, ids, lse, entropy, *up, dx, dc, dbias, bias, ctx.scale)
-        return dx, dc, dbias, None, None, None
+    def backward(ctx, *grads):
+        # a graph of the gradients is only recorded to refuse a second derivative
+        return (_backward_once if torch.is_grad_enabled() else _backward)(ctx, *grads)
 
 
 def token_log_probs(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0,
@@ -74,28 +87,29 @@ def token_log_probs(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, *, scal
     -inf masks an entry.  top <= min(K, 28) likeliest entries, lowest index on ties.
     logp, lse and entropy are fp32 and differentiable; top_ids and top_logp are not.
     """
-    if x.dim() < 1 or c.dim() not in (2, 3):
+    if x.dim() < 1 or c.dim() not in (2, 3) or (c.dim() == 3 and x.dim() != 3):
         raise ValueError("x must be (..., d) and c (K, d), or x (B, N, d) and c (B, K, d)")
-    lead = tuple(x.shape[:-1])
-    if tuple(ids.shape) != lead:
-        raise ValueError(f"ids must be {lead}, got {tuple(ids.shape)}")
+    lead = x.shape[:-1]
+    if ids.shape != lead:
+        raise ValueError(f"ids must be {tuple(lead)}, got {tuple(ids.shape)}")
     if ids.dtype == torch.int64:  # any value out of range stays out of range
-        ids = ids.clamp(-1, c.shape[-2])
+        ids = ids.clamp(-1, c.shape[-2]).int()
     elif ids.dtype != torch.int32:
         raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
-    if bias is not None:
+    if bias is not None and bias.dtype != torch.float32:
         bias = bias.float()
-    if c.dim() == 2:
-        xs, cs, ids = x.reshape(1, -1, x.shape[-1]), c.unsqueeze(0), ids.reshape(1, -1)
-        if bias is not None:
-            bias = bias.unsqueeze(0)
+    shared = c.dim() == 2
+    if shared:
+        x, c, ids = x.reshape(1, -1, x.shape[-1]), c.unsqueeze(0), ids.reshape(1, -1)
+        bias = None if bias is None else bias.unsqueeze(0)
+    x, c, ids = x.contiguous(), c.contiguous(), ids.contiguous()
+    bias = None if bias is None else bias.contiguous()
+    if torch.is_grad_enabled() and (x.requires_grad or c.requires_grad or (bias is not None and bias.requires_grad)):
+        out = _LogProbs.apply(x, c, bias, ids, float(scale), int(top))
     else:
-        xs, cs = x, c
-    if bias is not None:
-        bias = bias.contiguous()
-    out = _LogProbs.apply(xs.contiguous(), cs.contiguous(), bias, ids.int().contiguous(), float(scale), int(top))
-    if c.dim() == 2:
-        out = [None if t is None else t.reshape(lead + tuple(t.shape[2:])) for t in out]
+        out = _forward(x, c, bias, ids, float(scale), int(top))
+    if shared and (len(lead) != 2 or lead[0] != 1):
+        out = [None if t is None else t.reshape(lead + t.shape[2:]) for t in out]
     return TokenLogProbs(*out)
 
 
@@ -125,11 +139,14 @@ def expert_mixture(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_
         raise RuntimeError("expert_mixture has no backward pass: call it under torch.no_grad()")
     if x.dim() < 1:
         raise ValueError("x must be (..., d)")
-    lead = tuple(x.shape[:-1])
-    xs = x.reshape(-1, x.shape[-1]).contiguous()
+    k, lead, dev = int(top_k), x.shape[:-1], x.device
+    flat = x.dim() == 2
+    xs = (x if flat else x.reshape(-1, x.shape[-1])).contiguous()
     y = torch.empty_like(xs)
-    ids = torch.empty((xs.shape[0], int(top_k)), dtype=torch.int32, device=x.device)
-    weights = torch.empty((xs.shape[0], int(top_k)), dtype=torch.float32, device=x.device)
+    ids = torch.empty((xs.shape[0], k), dtype=torch.int32, device=dev)
+    weights = torch.empty((xs.shape[0], k), dtype=torch.float32, device=dev)
     fk_moe(xs, router.contiguous(), w_in.contiguous(), w_out.contiguous(), y, ids, weights, _ACTIVATIONS[activation],
            renormalize)
-    return ExpertMixture(y.reshape(x.shape), ids.reshape(lead + (int(top_k),)), weights.reshape(lead + (int(top_k),)))
+    if flat:
+        return ExpertMixture(y, ids, weights)
+    return ExpertMixture(y.reshape(x.shape), ids.reshape(lead + (k,)), weights.reshape(lead + (k,)))
