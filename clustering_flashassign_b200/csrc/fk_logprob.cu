@@ -76,16 +76,46 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
-// The 32 scores (base 2) of a thread's row in columns [col, col + 32) from the
-// accumulators.  A bias of -inf masks its column whatever the product holds.
+// A warp's bias of its half tile's 128 columns, times log2 e, in shared memory;
+// columns past the last count as masked.  `masked`: which of the four
+// 32-column chunks hold a masked column.
+struct BiasTile {
+  static constexpr int kFloats = 128;
+  float *sb;
+  unsigned masked = 0;
+  __device__ __forceinline__ void load(const float *bias, long long col0, long long K, int lane) {
+    __syncwarp();  // the previous tile's values have been read
+    masked = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long col = col0 + i * 32 + lane;
+      const float b = col < K ? __ldg(bias + col) : kNegInf;
+      sb[i * 32 + lane] = b * kLog2e;
+      if (__any_sync(0xffffffffu, b == kNegInf)) masked |= 1u << i;
+    }
+    __syncwarp();
+  }
+};
+
+// The 32 scores (base 2) of a thread's row in columns [col, col + 32), chunk i
+// of the half tile.  A bias of -inf masks its column whatever the product holds.
 template <bool BIAS>
-__device__ __forceinline__ void scores32(const float (&r)[32], float scale2, const float *bias, long long col,
+__device__ __forceinline__ void scores32(const float (&r)[32], float scale2, const BiasTile &bt, int i, long long col,
                                          long long K, float (&t)[32]) {
   if (BIAS) {
+    const float4 *sb = reinterpret_cast<const float4 *>(bt.sb + i * 32);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float b = col + j < K ? __ldg(bias + col + j) : kNegInf;
-      t[j] = b == kNegInf ? kNegInf : fmaf(r[j], scale2, b * kLog2e);
+    for (int j = 0; j < 8; ++j) {
+      const float4 b = sb[j];
+      t[4 * j] = fmaf(r[4 * j], scale2, b.x);
+      t[4 * j + 1] = fmaf(r[4 * j + 1], scale2, b.y);
+      t[4 * j + 2] = fmaf(r[4 * j + 2], scale2, b.z);
+      t[4 * j + 3] = fmaf(r[4 * j + 3], scale2, b.w);
+    }
+    if (bt.masked >> i & 1u) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (bt.sb[i * 32 + j] == kNegInf) t[j] = kNegInf;
     }
   } else {
 #pragma unroll
@@ -113,19 +143,24 @@ struct StatArgs {
 
 // Running statistics of one row per thread.
 //
-// The best columns: a 32-column chunk whose maximum beats the row's list is
-// drained from its maximum downwards, every lane inserting its own best column
-// in the same step, until no lane's remainder beats its list.  The steps of a
-// chunk are then the most columns that any of the 32 rows keeps of it (after
-// the first few hundred columns mostly none), where a scan in column order
-// would pay one insertion for nearly every column that any row wants.
-template <bool BIAS, bool TOP, bool SEG>
+// The sums refer to a maximum that follows the row's with a slack of 2^8: a
+// chunk's exponentials then rarely wait for its maximum.
+//
+// The best columns.  Eight columns of which no row of the warp wants anything
+// (their maximum beats none of the lists) cost a comparison.  Otherwise they
+// are drained from their maximum downwards, every lane inserting its own best
+// column in the same step, until no lane's remainder beats its list.  A list of
+// 8 or 16 (LREG) sits in registers, where an insertion is a branchless shift of
+// five instructions a place; a longer one in shared memory.
+template <bool BIAS, bool TOP, int LREG, bool SEG>
 struct StatEpi {
   using Args = StatArgs;
   static constexpr bool kSeg = SEG;
   static constexpr int kSlots = 32 * tile::kEpiWarps;
+  static constexpr int kCap = LREG ? LREG : 1;
   const Args &a;
-  const int r, half, slot;
+  const int r, half, slot, lane;
+  BiasTile bt;
   float *lv;
   int32_t *li;
   const float *bias = nullptr;
@@ -133,11 +168,21 @@ struct StatEpi {
   int id = -1;
   bool idle = false;  // none of the warp's rows exists
   float m = 0.f, sum = 0.f, us = 0.f, tgt = 0.f, thr = 0.f;
+  float rv[kCap];
+  int rk[kCap];
 
-  __device__ StatEpi(const Args &args, int lane, int r_in_tile, int half_, uint8_t *smem)
-      : a(args), r(r_in_tile), half(half_), slot(half_ * 128 + r_in_tile) {
-    lv = reinterpret_cast<float *>(smem) + slot;
-    li = reinterpret_cast<int32_t *>(smem) + args.L * kSlots + slot;
+  __device__ StatEpi(const Args &args, int lane_, int r_in_tile, int half_, uint8_t *smem)
+      : a(args), r(r_in_tile), half(half_), slot(half_ * 128 + r_in_tile), lane(lane_) {
+    float *f = reinterpret_cast<float *>(smem);
+    if (BIAS) {
+      bt.sb = f + (slot / 32) * BiasTile::kFloats;
+      f += tile::kEpiWarps * BiasTile::kFloats;
+    }
+    lv = f + slot;
+    li = reinterpret_cast<int32_t *>(f) + args.L * kSlots + slot;
+  }
+  static size_t smem_bytes(int L) {
+    return (BIAS ? tile::kEpiWarps * BiasTile::kFloats * 4 : 0) + (TOP && !LREG ? (size_t)L * kSlots * 8 : 0);
   }
 
   __device__ void begin(const Unit &w, long long row0) {
@@ -149,12 +194,23 @@ struct StatEpi {
     m = thr = tgt = kNegInf;
     sum = us = 0.f;
     if (TOP) {
-      for (int j = 0; j < a.L; ++j) {
-        lv[j * kSlots] = kNegInf;
-        li[j * kSlots] = -1;
+      if (LREG) {
+#pragma unroll
+        for (int j = 0; j < kCap; ++j) {
+          rv[j] = kNegInf;
+          rk[j] = -1;
+        }
+      } else {
+        for (int j = 0; j < a.L; ++j) {
+          lv[j * kSlots] = kNegInf;
+          li[j * kSlots] = -1;
+        }
       }
       if (row >= a.N) thr = INFINITY;  // a row beyond the last keeps nothing
     }
+  }
+  __device__ __forceinline__ void prepare(long long col0) {
+    if (BIAS && !skip(col0)) bt.load(bias, col0, a.K, lane);
   }
 
   __device__ __forceinline__ void insert(float v, int k) {
@@ -170,18 +226,48 @@ struct StatEpi {
     thr = lv[(a.L - 1) * kSlots];
   }
 
-  static __device__ __forceinline__ float max32(const float (&t)[32]) {
-    float cm = max3(t[0], t[1], t[2]);
+  // Into the register list (descending; an equal value that came earlier, from
+  // lower columns, stays ahead).  v = -inf inserts nothing.
+  __device__ __forceinline__ void insert_reg(float v, int k) {
 #pragma unroll
-    for (int j = 3; j < 31; j += 2) cm = max3(cm, t[j], t[j + 1]);
-    return fmaxf(cm, t[31]);
+    for (int i = kCap - 1; i >= 0; --i) {
+      const bool below = v > rv[i];
+      const bool shift = i > 0 && v > rv[i > 0 ? i - 1 : 0];
+      rk[i] = below ? (shift ? rk[i > 0 ? i - 1 : 0] : k) : rk[i];
+      rv[i] = i > 0 ? fmaxf(rv[i], fminf(rv[i > 0 ? i - 1 : 0], v)) : fmaxf(rv[i], v);
+    }
+    if (row < a.N) thr = rv[kCap - 1];
   }
 
-  __device__ __forceinline__ void chunk(const float (&acc)[32], long long col) {
+  // Eight consecutive columns, m8 their maximum.
+  __device__ __forceinline__ void drain8(float *t, float m8, int col) {
+    while (__any_sync(0xffffffffu, m8 > thr)) {
+      const bool take = m8 > thr;
+      int j8 = 8;
+#pragma unroll
+      for (int j = 7; j >= 0; --j)
+        if (t[j] == m8) j8 = j;
+      if (LREG) insert_reg(take ? m8 : kNegInf, col + j8);
+      else if (take) insert(m8, col + j8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j == j8) t[j] = kNegInf;
+      __syncwarp();
+      m8 = max3(max3(t[0], t[1], t[2]), max3(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
+    }
+  }
+
+  __device__ __forceinline__ void chunk(const float (&acc)[32], long long col, int i) {
     float t[32];
-    scores32<BIAS>(acc, a.scale2, bias, col, a.K, t);
-    float cm = max32(t);
-    if (cm > m) {
+    scores32<BIAS>(acc, a.scale2, bt, i, col, a.K, t);
+    float g[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float *v = t + 8 * q;
+      g[q] = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), fmaxf(v[6], v[7]));
+    }
+    const float cm = max3(fmaxf(g[0], g[1]), g[2], g[3]);
+    if (cm > m + 8.f) {  // always the case for the first finite chunk
       if (m != kNegInf) {
         const float f = ex2(m - cm);
         us = f * fmaf(m - cm, sum, us);
@@ -208,20 +294,9 @@ struct StatEpi {
       for (int j = 0; j < 32; ++j)
         if (rel == (unsigned)j) tgt = t[j];
     }
-    if (TOP) {
-      while (__any_sync(0xffffffffu, cm > thr)) {
-        const bool take = cm > thr;
-        int at_j = -1;
+    if (TOP && __any_sync(0xffffffffu, cm > thr)) {
 #pragma unroll
-        for (int j = 31; j >= 0; --j)
-          if (t[j] == cm) at_j = j;
-        if (take) insert(cm, (int)col + at_j);
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j == at_j) t[j] = kNegInf;
-        __syncwarp();
-        cm = max32(t);
-      }
+      for (int q = 0; q < 4; ++q) drain8(t + 8 * q, g[q], (int)col + 8 * q);
     }
   }
 
@@ -229,11 +304,18 @@ struct StatEpi {
     if (row >= a.N) return;
     const long long p = at * a.parts + w.run * 2 + half;
     a.part[p] = make_float4(m, sum, us, tgt);
-    if (TOP)
+    if (TOP && LREG) {
+#pragma unroll
+      for (int j = 0; j < kCap; j += 4) {
+        reinterpret_cast<float4 *>(a.top_v + p * kCap)[j / 4] = make_float4(rv[j], rv[j + 1], rv[j + 2], rv[j + 3]);
+        reinterpret_cast<int4 *>(a.top_i + p * kCap)[j / 4] = make_int4(rk[j], rk[j + 1], rk[j + 2], rk[j + 3]);
+      }
+    } else if (TOP) {
       for (int j = 0; j < a.L; ++j) {
         a.top_v[p * a.L + j] = lv[j * kSlots];
         a.top_i[p * a.L + j] = li[j * kSlots];
       }
+    }
   }
   __device__ __forceinline__ bool skip(long long col) const { return idle || col >= a.K; }
 };
@@ -248,7 +330,7 @@ struct JoinArgs {
   const float *bias;
   float scale;
   long long rows, N, K;
-  int d, parts, L, top;
+  int d, parts, L, cands, top;  // L: length of a partial list; cands = min(K, L)
   bool vec;  // rows of x and c can be read 16 bytes at a time
   float *logp, *lse, *entropy, *top_logp;
   int32_t *top_ids;
@@ -482,9 +564,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
   if (sub == 0) {
     // masked (or NaN) columns are in no list: they follow, lowest index first
     const int found = __popc(__ballot_sync(0xffffffffu, mine >= 0) & mask);
-    if (__any_sync(0xffffffffu, found < a.L)) {
+    if (__any_sync(0xffffffffu, found < a.cands)) {
       int next = 0;
-      for (int j = 0; j < a.L; ++j) {
+      for (int j = 0; j < a.cands; ++j) {
         const bool fill = j >= found;
         for (;;) {
           const bool listed = fill & ((__ballot_sync(0xffffffffu, mine == next) & mask) != 0u);
@@ -504,34 +586,34 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
   const T *c = static_cast<const T *>(a.c) + (size_t)b * a.K * a.d;
   const float *bias = a.bias ? a.bias + b * a.K : nullptr;
   double v = (double)kNegInf;
-  for (int j = 4 * sub; j < a.L; j += 4 * WPR) {
+  for (int j = 4 * sub; j < a.cands; j += 4 * WPR) {
     int k[4];
     double e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int src = min(j + i, a.L - 1);
+      const int src = min(j + i, a.cands - 1);
       k[i] = WPR > 1 ? sh.cand[src] : __shfl_sync(0xffffffffu, mine, src, LPR);
     }
     exact_scores<T, LPR>(x, c, bias, a.scale, k, a.d, a.vec, lane, e);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (lane == j + i) v = e[i];
-      if (WPR > 1 && lane == 0 && j + i < a.L) sh.exact[j + i] = e[i];
+      if (WPR > 1 && lane == 0 && j + i < a.cands) sh.exact[j + i] = e[i];
     }
   }
   if (WPR > 1) {
     __syncthreads();
     if (warp != 0) return;
-    if (lane < a.L) v = sh.exact[lane];
+    if (lane < a.cands) v = sh.exact[lane];
   }
   const double rank_v = v == v ? v : (double)kNegInf;
   int rank = 0;
-  for (int j = 0; j < a.L; ++j) {
+  for (int j = 0; j < a.cands; ++j) {
     const double v2 = __shfl_sync(0xffffffffu, rank_v, j, LPR);
     const int k2 = __shfl_sync(0xffffffffu, mine, j, LPR);
     rank += v2 > rank_v || (v2 == rank_v && k2 < mine);
   }
-  if (live && lane < a.L && rank < a.top) {
+  if (live && lane < a.cands && rank < a.top) {
     a.top_ids[r * a.top + rank] = mine;
     a.top_logp[r * a.top + rank] = v == (double)kNegInf && s == s ? kNegInf
                                                                   : (float)(v - (double)(none ? kNegInf : m) * M_LN2) -
@@ -603,6 +685,7 @@ struct GradEpi {
   static constexpr bool kSeg = SEG;
   const Args &a;
   const int r, lane;
+  BiasTile bt;
   const float *bias = nullptr;
   RowGrad q = {};
   long long row = 0;
@@ -610,7 +693,9 @@ struct GradEpi {
   T *g = nullptr;
   float *cp = nullptr;
 
-  __device__ GradEpi(const Args &args, int lane_, int r_in_tile, int, uint8_t *) : a(args), r(r_in_tile), lane(lane_) {
+  __device__ GradEpi(const Args &args, int lane_, int r_in_tile, int half, uint8_t *smem)
+      : a(args), r(r_in_tile), lane(lane_) {
+    bt.sb = reinterpret_cast<float *>(smem) + (half * 4 + r_in_tile / 32) * BiasTile::kFloats;
     if (args.bound) gs = grad_scale(*args.bound);
   }
   __device__ void begin(const Unit &w, long long row0) {
@@ -623,11 +708,15 @@ struct GradEpi {
     const long long blk = (row0 + (r & ~31)) >> 5;
     cp = a.colpart && blk < a.nblk ? a.colpart + (w.b * a.nblk + blk) * a.Kp : nullptr;
   }
+  static size_t smem_bytes() { return BIAS ? tile::kEpiWarps * BiasTile::kFloats * 4 : 0; }
+  __device__ __forceinline__ void prepare(long long col0) {
+    if (BIAS) bt.load(bias, col0, a.K, lane);
+  }
   __device__ __forceinline__ bool skip(long long col) const { return col >= a.Kp; }
-  __device__ __forceinline__ void chunk(const float (&acc)[32], long long col) {
+  __device__ __forceinline__ void chunk(const float (&acc)[32], long long col, int i) {
     {
       float v[32];
-      scores32<BIAS>(acc, a.scale2, bias, col, a.K, v);
+      scores32<BIAS>(acc, a.scale2, bt, i, col, a.K, v);
       const int rel = q.id - (int)col;
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
@@ -733,8 +822,9 @@ struct StoreEpi {
     out = static_cast<T *>(a.out) + w.b * a.batch_stride + row * a.pitch;
     if (a.part) part = a.part + w.ks * a.slot + (w.b * a.rows + row) * a.cols;
   }
+  __device__ __forceinline__ void prepare(long long) {}
   __device__ __forceinline__ bool skip(long long col) const { return col >= a.cols; }
-  __device__ __forceinline__ void chunk(const float (&acc)[32], long long col) {
+  __device__ __forceinline__ void chunk(const float (&acc)[32], long long col, int) {
     if (row >= a.rows) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -977,6 +1067,10 @@ struct Carve {
   }
 };
 
+// Columns a partial list keeps: at least kSpare more than asked for, 8 or 16 in
+// registers, else 32 in shared memory.
+int list_length(int top) { return top == 0 ? 0 : top + kSpare <= 8 ? 8 : top + kSpare <= 16 ? 16 : 32; }
+
 struct FwdSpace {
   Plan p;
   int L;
@@ -990,7 +1084,7 @@ struct FwdSpace {
 FwdSpace fwd_space(const Dims &m, int top, void *base) {
   FwdSpace f = {};
   f.p = plan_runs(m.B, m.N, m.K, m.d, m.pairs, m.planes, m.dp * 2 * m.planes);
-  f.L = top ? std::min(m.K, top + kSpare) : 0;
+  f.L = list_length(top);
   Carve w(base);
   const long long parts = 2LL * f.p.runs;
   f.part = (float4 *)w.take((size_t)m.B * m.N * parts * sizeof(float4));
@@ -1020,12 +1114,19 @@ int operand(const void *src, int dtype, long long rows, long long rows_per_b, in
   return launch_operand<__half>(src, rows, rows_per_b, d, dp, g, bias, dst, s);  // 16-bit rows are copied as bits
 }
 
+template <class Epi>
+int stats_as(const CUtensorMap &tx, const CUtensorMap &tc, const FwdSpace &f, const StatArgs &a, int fmt, int *err,
+             cudaStream_t s) {
+  return launch_tiles<Epi, false, false>(tx, tc, f.p, a, Epi::smem_bytes(f.L), fmt, err, s);
+}
+
 template <bool BIAS, bool SEG>
 int stats_seg(const CUtensorMap &tx, const CUtensorMap &tc, const FwdSpace &f, const StatArgs &a, int fmt, int *err,
               cudaStream_t s) {
-  const size_t lists = (size_t)f.L * StatEpi<BIAS, true, SEG>::kSlots * 8;
-  if (f.L) return launch_tiles<StatEpi<BIAS, true, SEG>, false, false>(tx, tc, f.p, a, lists, fmt, err, s);
-  return launch_tiles<StatEpi<BIAS, false, SEG>, false, false>(tx, tc, f.p, a, 0, fmt, err, s);
+  if (f.L == 0) return stats_as<StatEpi<BIAS, false, 0, SEG>>(tx, tc, f, a, fmt, err, s);
+  if (f.L == 8) return stats_as<StatEpi<BIAS, true, 8, SEG>>(tx, tc, f, a, fmt, err, s);
+  if (f.L == 16) return stats_as<StatEpi<BIAS, true, 16, SEG>>(tx, tc, f, a, fmt, err, s);
+  return stats_as<StatEpi<BIAS, true, 0, SEG>>(tx, tc, f, a, fmt, err, s);
 }
 
 template <bool BIAS>
@@ -1133,9 +1234,9 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
       // scores as exact as the forward pass's where fp32 results hang on them;
       // a 16-bit gradient does not show the difference (2^-15 against 2^-9)
       if ((m.planes == 3 || dbias) && pg.kblocks * pg.pairs > tile::kSegBlocks)
-        FK_TRY((launch_tiles<GradEpi<G, BIAS, true>, false, false>(tx, tc, pg, ga, 0, fmt, err, s)));
+        FK_TRY((launch_tiles<GradEpi<G, BIAS, true>, false, false>(tx, tc, pg, ga, GradEpi<G, BIAS, true>::smem_bytes(), fmt, err, s)));
       else
-        FK_TRY((launch_tiles<GradEpi<G, BIAS, false>, false, false>(tx, tc, pg, ga, 0, fmt, err, s)));
+        FK_TRY((launch_tiles<GradEpi<G, BIAS, false>, false, false>(tx, tc, pg, ga, GradEpi<G, BIAS, false>::smem_bytes(), fmt, err, s)));
       if (dbias) {
         FK_CUDA(launch_pdl(k_sum_cols, dim3((unsigned)cdiv(m.K, 32), bn), dim3(256), 0, s, (const float *)f.colpart,
                            ga.nblk, m.Kp, (long long)m.K, dbias + (size_t)b0 * m.K, r0 > 0 ? 1 : 0));
@@ -1286,7 +1387,7 @@ int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float 
   j.part = f.part, j.top_v = f.top_v, j.top_i = f.top_i;
   j.ids = ids, j.x = x, j.c = c, j.bias = bias, j.scale = scale;
   j.rows = m.B * m.N, j.N = m.N, j.K = m.K, j.d = m.d;
-  j.parts = a.parts, j.L = f.L, j.top = top;
+  j.parts = a.parts, j.L = f.L, j.cands = std::min(f.L, m.K), j.top = top;
   j.logp = logp, j.lse = lse, j.entropy = entropy, j.top_logp = top_logp, j.top_ids = top_ids;
   j.err = err;
   j.vec = m.d * esize(m.dtype) % 16 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(c)) & 15) == 0;

@@ -200,6 +200,22 @@ __device__ __forceinline__ void tmem_dealloc_cg(uint32_t addr, uint32_t n) {
   else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(n) : "memory");
 }
 
+// Waits for this thread's TMEM loads; the registers they fill pass through, so
+// that no use of them can be moved ahead of the wait.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
 // All lanes return the same verdict of a wait that lane 0 polls.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err,
                                           int lane) {
@@ -213,7 +229,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 //   static constexpr bool kSeg     sum segments of the contraction in registers
 //   begin(const Unit &, row0)      before the unit's first tile
 //   skip(column)                   warp-uniform: nothing to do from this column on
-//   chunk(32 values, column)       the row's values of 32 consecutive columns
+//   prepare(column)                before the wait for a tile's products
+//   chunk(32 values, column, i)    the row's values of the half tile's i-th 32 columns
 //   end(const Unit &)              after the unit's last tile
 // and is constructed per thread with (args, lane, row in CTA tile, half, shared memory).
 template <int CG, bool A_MN, bool B_MN, class Epi>
@@ -377,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int ct = w.ct0; ct < w.ct1 && ok; ++ct) {
         const long long col0 = (long long)ct * kCols + half * (kCols / 2);
         const uint32_t lanes = tmem + half * (kCols / 2) + ((uint32_t)(quad * 32) << 16);
+        epi.prepare(col0);
         if constexpr (Epi::kSeg) {
           float sum[4][32];
 #pragma unroll
@@ -392,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t acc[32];
               if (!epi.skip(col0 + ch * 32)) {
                 tmem_ld_32x32b_x32(lanes + buf * kCols + ch * 32, acc);
-                tmem_wait_ld();
+                wait_ld(acc);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) sum[ch][j] += __uint_as_float(acc[j]);
               }
@@ -400,24 +418,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             release(buf);
           }
           if (ok) {
+            // one copy of the epilogue's code: the sums move up instead
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+              if (epi.skip(col0 + ch * 32)) break;
+              epi.chunk(sum[0], col0 + ch * 32, ch);
+              __syncwarp();
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-              if (!epi.skip(col0 + ch * 32)) {
-                epi.chunk(sum[ch], col0 + ch * 32);
-                __syncwarp();
-              }
+              for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[i][j] = sum[i + 1][j];
+            }
           }
         } else {
           const uint32_t buf = n & 1;
           if (!warp_wait(tfull(buf), (n >> 1) & 1, abort_flag, err, lane)) { ok = false; break; }
           tc_fence_after();
+          // the next 32 columns travel while these are worked on
+          uint32_t next[32];
+          if (!epi.skip(col0)) tmem_ld_32x32b_x32(lanes + buf * kCols, next);
 #pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
             if (epi.skip(col0 + ch * 32)) break;
             float acc[32];
-            tmem_ld_32x32b_x32(lanes + buf * kCols + ch * 32, reinterpret_cast<uint32_t(&)[32]>(acc));
-            tmem_wait_ld();
-            epi.chunk(acc, col0 + ch * 32);
+            wait_ld(next);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[j] = __uint_as_float(next[j]);
+            if (ch < 3 && !epi.skip(col0 + ch * 32 + 32))
+              tmem_ld_32x32b_x32(lanes + buf * kCols + ch * 32 + 32, next);
+            epi.chunk(acc, col0 + ch * 32, ch);
             __syncwarp();  // the next load is warp-wide
           }
           release(buf);
