@@ -1,0 +1,332 @@
+// Joins the partial results of the score kernels, row by row.
+#include "fk_logprob.cuh"
+
+namespace fk {
+namespace soft {
+namespace {
+
+__device__ __forceinline__ void join_stats(float &m, float &s, float &u, float m2, float s2, float u2) {
+  const float mm = fmaxf(m, m2);
+  const float ms = mm == kNegInf ? 0.f : mm;
+  // an empty side has s = u = 0 and its (clamped) distance contributes nothing;
+  // a NaN sum stays NaN
+  const float d1 = fmaxf(m - ms, kLowest), d2 = fmaxf(m2 - ms, kLowest);
+  const float f1 = ex2(m - ms), f2 = ex2(m2 - ms);
+  u = f1 * fmaf(d1, s, u) + f2 * fmaf(d2, s2, u2);
+  s = f1 * s + f2 * s2;
+  m = mm;
+}
+
+// Scores of C columns in fp64, by LPR lanes, from the operands as given:
+// products of 16-bit values are exact, and fp64 sums keep neighbours in rank
+// apart that the fp32 accumulation cannot.
+template <typename T, int LPR, int C>
+__device__ __forceinline__ void exact_scores(const T *x, const T *c, const float *bias, float scale, const int (&k)[C],
+                                             int d, bool vec, int lane, double (&s)[C]) {
+#pragma unroll
+  for (int i = 0; i < C; ++i) s[i] = 0.0;
+  constexpr int V = 16 / sizeof(T);
+  if (vec) {
+#pragma unroll(C == 1 ? 4 : 2)
+    for (int j = lane; j < d / V; j += LPR) {
+      T xv[V], cv[C][V];
+      *reinterpret_cast<uint4 *>(xv) = __ldg(reinterpret_cast<const uint4 *>(x) + j);
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        *reinterpret_cast<uint4 *>(cv[i]) = __ldg(reinterpret_cast<const uint4 *>(c + (size_t)k[i] * d) + j);
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const double xd = (double)to_f(xv[q]);
+#pragma unroll
+        for (int i = 0; i < C; ++i) s[i] = fma(xd, (double)to_f(cv[i][q]), s[i]);
+      }
+    }
+  } else {
+    for (int j = lane; j < d; j += LPR) {
+      const double xd = (double)to_f(x[j]);
+#pragma unroll
+      for (int i = 0; i < C; ++i) s[i] = fma(xd, (double)to_f(c[(size_t)k[i] * d + j]), s[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+    s[i] *= (double)scale;
+    if (bias) s[i] = bias[k[i]] == kNegInf ? (double)kNegInf : s[i] + (double)bias[k[i]];
+  }
+}
+
+constexpr int kJoinWarps = 8;
+constexpr int kNoCol = 0x7fffffff;
+
+// One warp's joined lists (and the row's candidates with their exact scores)
+// where eight warps share a row.
+struct JoinRow {
+  float m[kJoinWarps], s[kJoinWarps], u[kJoinWarps], tgt[kJoinWarps];
+  float v[kJoinWarps][32];
+  int k[kJoinWarps][32];
+  int cand[32];
+  double exact[32];
+};
+
+// The best `n` of the lanes' sorted lists of up to LL columns (k < 0: the end);
+// lane j of the group keeps the j-th.  The lists move up as their heads go.
+template <int LPR, int LL>
+__device__ __forceinline__ void draw(int n, int lane, float (&lv)[LL], int (&lk)[LL], float &mv, int &mk) {
+  mv = kNegInf;
+  mk = -1;
+  for (int j = 0; j < n; ++j) {
+    float v = lk[0] >= 0 ? lv[0] : kNegInf;
+    int k = lk[0] >= 0 ? lk[0] : kNoCol;
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) {
+      const float v2 = __shfl_xor_sync(0xffffffffu, v, o);
+      const int k2 = __shfl_xor_sync(0xffffffffu, k, o);
+      if (v2 > v || (v2 == v && k2 < k)) {
+        v = v2;
+        k = k2;
+      }
+    }
+    if (lane == j && k != kNoCol) {
+      mv = v;
+      mk = k;
+    }
+    const bool won = lk[0] == k;
+#pragma unroll
+    for (int i = 0; i < LL; ++i) {
+      lv[i] = won && i + 1 < LL ? lv[i + 1 < LL ? i + 1 : i] : lv[i];
+      lk[i] = won ? (i + 1 < LL ? lk[i + 1 < LL ? i + 1 : i] : -1) : lk[i];
+    }
+  }
+}
+
+// LPR lanes of WPR warps per row.  (8, 1): many rows of few parts, four rows a
+// warp; (32, 1); (32, 8): few rows, whose exact scores would otherwise be one
+// warp's long chain of loads.
+template <typename T, int LPR, int WPR, int LL>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
+  __shared__ JoinRow sh;
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & (LPR - 1);
+  const int sub = WPR > 1 ? warp : 0;  // this warp among the row's warps
+  const long long per_block = WPR > 1 ? 1 : kJoinWarps * (32 / LPR);
+  const long long r0 = (long long)blockIdx.x * per_block + (WPR > 1 ? 0 : threadIdx.x / LPR);
+  // lanes of a row beyond the last one follow along on the last row
+  const bool live = r0 < a.rows;
+  const long long r = live ? r0 : a.rows - 1;
+  const long long b = r / a.N;
+  const int first = sub * LPR + lane, step = LPR * WPR;
+  float m = kNegInf, s = 0.f, u = 0.f, tgt = kNegInf;
+  for (int p = first; p < a.parts; p += step) {
+    const float4 q = a.part[r * a.parts + p];
+    join_stats(m, s, u, q.x, q.y, q.z);
+    tgt = fmaxf(tgt, q.w);
+  }
+#pragma unroll
+  for (int o = LPR / 2; o; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    const float u2 = __shfl_xor_sync(0xffffffffu, u, o);
+    // both sides join in the same order, so that all lanes hold the same bits
+    if (lane & o) {
+      float mm = m2, ss = s2, uu = u2;
+      join_stats(mm, ss, uu, m, s, u);
+      m = mm, s = ss, u = uu;
+    } else {
+      join_stats(m, s, u, m2, s2, u2);
+    }
+    tgt = fmaxf(tgt, __shfl_xor_sync(0xffffffffu, tgt, o));
+  }
+  if (WPR > 1) {
+    if (lane == 0) {
+      sh.m[warp] = m, sh.s[warp] = s, sh.u[warp] = u, sh.tgt[warp] = tgt;
+    }
+    __syncthreads();
+    m = sh.m[0], s = sh.s[0], u = sh.u[0], tgt = sh.tgt[0];
+    for (int w = 1; w < WPR; ++w) {
+      join_stats(m, s, u, sh.m[w], sh.s[w], sh.u[w]);
+      tgt = fmaxf(tgt, sh.tgt[w]);
+    }
+  }
+  // a row whose columns are all masked has lse = -inf and an entropy of zero
+  const bool none = m == kNegInf && s == 0.f;
+  const float ls = log2f(s);
+  if (live && lane == 0 && sub == 0) {
+    const int id = a.ids[r];
+    const bool valid = id >= 0 && id < a.K;
+    if (id >= a.K) atomicCAS(a.err, DEV_OK, DEV_BAD_ID);
+    a.lse[r] = none ? kNegInf : (m + ls) * kLn2;
+    if (a.entropy) a.entropy[r] = none ? 0.f : (ls - u / s) * kLn2;
+    a.logp[r] = !valid ? 0.f : (none || (tgt == kNegInf && s == s)) ? kNegInf : ((tgt - m) - ls) * kLn2;
+  }
+  if (a.top == 0) return;
+
+  // the lane's own list: its parts' lists, joined (LL columns at most)
+  float hv[LL], mv;
+  int hk[LL], mine;
+#pragma unroll
+  for (int i = 0; i < LL; ++i) {
+    hv[i] = kNegInf;
+    hk[i] = -1;
+  }
+  for (int p = first; p < a.parts; p += step) {
+    const float4 *pv = reinterpret_cast<const float4 *>(a.top_v + (r * a.parts + p) * a.L);
+    const int4 *pk = reinterpret_cast<const int4 *>(a.top_i + (r * a.parts + p) * a.L);
+    float nv[LL];
+    int nk[LL];
+#pragma unroll
+    for (int i = 0; i < LL / 4; ++i) {
+      const float4 v = __ldg(pv + i);
+      const int4 k = __ldg(pk + i);
+      nv[4 * i] = v.x, nv[4 * i + 1] = v.y, nv[4 * i + 2] = v.z, nv[4 * i + 3] = v.w;
+      nk[4 * i] = k.x, nk[4 * i + 1] = k.y, nk[4 * i + 2] = k.z, nk[4 * i + 3] = k.w;
+    }
+    if (p == first) {
+#pragma unroll
+      for (int i = 0; i < LL; ++i) {
+        hv[i] = nv[i];
+        hk[i] = nk[i];
+      }
+    } else {
+#pragma unroll(LL <= 16 ? LL : 1)
+      for (int j = 0; j < LL; ++j) {
+        const float v = nv[j];
+        const unsigned k = (unsigned)nk[j];  // the end of a list orders after every column
+        // place it behind what is better: larger, or equal in a lower column
+#pragma unroll
+        for (int i = LL - 1; i >= 0; --i) {
+          const bool below = v > hv[i] || (v == hv[i] && k < (unsigned)hk[i]);
+          const bool shift = i > 0 && (v > hv[i > 0 ? i - 1 : 0] ||
+                                       (v == hv[i > 0 ? i - 1 : 0] && k < (unsigned)hk[i > 0 ? i - 1 : 0]));
+          hv[i] = below ? (shift ? hv[i > 0 ? i - 1 : 0] : v) : hv[i];
+          hk[i] = below ? (shift ? hk[i > 0 ? i - 1 : 0] : (int)k) : hk[i];
+        }
+      }
+    }
+  }
+  draw<LPR, LL>(a.cands, lane, hv, hk, mv, mine);
+  if (WPR > 1) {
+    sh.v[warp][lane] = mv;
+    sh.k[warp][lane] = mine;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 0; i < LL; ++i) {
+        hv[i] = lane < WPR ? sh.v[lane < WPR ? lane : 0][i] : kNegInf;
+        hk[i] = lane < WPR ? sh.k[lane < WPR ? lane : 0][i] : -1;
+      }
+      draw<LPR, LL>(a.cands, lane, hv, hk, mv, mine);
+    }
+  }
+  const unsigned group = LPR == 32 ? 0u : (threadIdx.x & 31) & ~(LPR - 1u);  // first lane of the row's group
+  const unsigned mask = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << group;
+  if (sub == 0) {
+    // masked (or NaN) columns are in no list: they follow, lowest index first
+    const int found = __popc(__ballot_sync(0xffffffffu, mine >= 0) & mask);
+    if (__any_sync(0xffffffffu, found < a.cands)) {
+      int next = 0;
+      for (int j = 0; j < a.cands; ++j) {
+        const bool fill = j >= found;
+        for (;;) {
+          const bool listed = fill & ((__ballot_sync(0xffffffffu, mine == next) & mask) != 0u);
+          if (!__any_sync(0xffffffffu, listed)) break;
+          next += listed;
+        }
+        if (fill && lane == j) mine = next;
+        if (fill) ++next;
+      }
+    }
+  }
+  if (WPR > 1) {
+    if (warp == 0) sh.cand[lane] = mine;
+    __syncthreads();
+  }
+  const T *x = static_cast<const T *>(a.x) + (size_t)r * a.d;
+  const T *c = static_cast<const T *>(a.c) + (size_t)b * a.K * a.d;
+  const float *bias = a.bias ? a.bias + b * a.K : nullptr;
+  double v = (double)kNegInf;
+  if (WPR > 1) {  // candidates warp, warp + 8, ...
+    if (warp < a.cands) {
+      int k[4];
+      double e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = sh.cand[warp + 8 * i < a.cands ? warp + 8 * i : warp];
+      if (a.cands <= 8) {
+        const int k1[1] = {k[0]};
+        double e1[1];
+        exact_scores<T, LPR, 1>(x, c, bias, a.scale, k1, a.d, a.vec, lane, e1);
+        e[0] = e1[0];
+      } else {
+        exact_scores<T, LPR, 4>(x, c, bias, a.scale, k, a.d, a.vec, lane, e);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lane == 0 && warp + 8 * i < a.cands) sh.exact[warp + 8 * i] = e[i];
+    }
+  } else {
+    for (int j = 0; j < a.cands; j += 4) {
+      int k[4];
+      double e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = __shfl_sync(0xffffffffu, mine, min(j + i, a.cands - 1), LPR);
+      exact_scores<T, LPR, 4>(x, c, bias, a.scale, k, a.d, a.vec, lane, e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lane == j + i) v = e[i];
+    }
+  }
+  if (WPR > 1) {
+    __syncthreads();
+    if (warp != 0) return;
+    if (lane < a.cands) v = sh.exact[lane];
+  }
+  const double rank_v = v == v ? v : (double)kNegInf;
+  int rank = 0;
+  for (int j = 0; j < a.cands; ++j) {
+    const double v2 = __shfl_sync(0xffffffffu, rank_v, j, LPR);
+    const int k2 = __shfl_sync(0xffffffffu, mine, j, LPR);
+    rank += v2 > rank_v || (v2 == rank_v && k2 < mine);
+  }
+  if (live && lane < a.cands && rank < a.top) {
+    a.top_ids[r * a.top + rank] = mine;
+    a.top_logp[r * a.top + rank] = v == (double)kNegInf && s == s ? kNegInf
+                                                                  : (float)(v - (double)(none ? kNegInf : m) * M_LN2) -
+                                                                        ls * kLn2;
+  }
+}
+
+template <typename T, int LPR, int WPR, int LL>
+int launch_join_as(const JoinArgs &j, cudaStream_t s) {
+  const int per_block = WPR > 1 ? 1 : kJoinWarps * (32 / LPR);
+  FK_CUDA(launch_pdl(k_join<T, LPR, WPR, LL>, dim3((unsigned)cdiv(j.rows, per_block)), dim3(32 * kJoinWarps), 0, s, j));
+  return launched();
+}
+
+// As many lanes per row as there are candidates (and more for many parts), at
+// least 8; a block per row while the rows alone do not fill the SMs.
+template <typename T, int LL>
+int launch_join_list(const JoinArgs &j, cudaStream_t s) {
+  if (j.L && j.rows <= 4096) return launch_join_as<T, 32, 8, LL>(j, s);
+  if (j.cands <= 8 && j.parts <= 64) return launch_join_as<T, 8, 1, LL>(j, s);
+  if (j.cands <= 16) return launch_join_as<T, 16, 1, LL>(j, s);
+  return launch_join_as<T, 32, 1, LL>(j, s);
+}
+
+template <typename T>
+int launch_join_typed(const JoinArgs &j, cudaStream_t s) {
+  if (j.L <= 4) return launch_join_list<T, 4>(j, s);
+  if (j.L == 8) return launch_join_list<T, 8>(j, s);
+  if (j.L <= 16) return j.L == 12 ? launch_join_list<T, 12>(j, s) : launch_join_list<T, 16>(j, s);
+  return launch_join_list<T, 32>(j, s);
+}
+
+}  // namespace
+
+int launch_join(const JoinArgs &j, int dtype, cudaStream_t s) {
+  if (dtype == FK_F32) return launch_join_typed<float>(j, s);
+  if (dtype == FK_BF16) return launch_join_typed<__nv_bfloat16>(j, s);
+  return launch_join_typed<__half>(j, s);
+}
+
+}  // namespace soft
+}  // namespace fk

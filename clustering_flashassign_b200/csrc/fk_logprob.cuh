@@ -1,0 +1,347 @@
+// Token log probabilities (the soft form of the assignment) and their
+// gradients.
+//
+//   s_nk  = scale * x_n . c_k + bias_k
+//   lse_n = log sum_k exp(s_nk),  p_nk = exp(s_nk - lse_n)
+//   logp_n = s_{n, id_n} - lse_n,  H_n = -sum_k p_nk log p_nk
+//   top:  the largest s_nk, lowest k on ties
+//   G_nk  = dL/ds_nk = a_n (1[k = id_n] - p_nk) + l_n p_nk - e_n p_nk (log p_nk + H_n)
+//           for the upstream gradients a, l, e of logp, lse and H,
+//   dx = scale * G C,  dc = scale * G^T X,  dbias_k = sum_n G_nk.
+//
+// The (B, N, K) scores never reach memory in the forward pass, as the distance
+// matrix never does in FlashAssign: every 128 x 256 tile of them is read once
+// from TMEM by the epilogue, which keeps the running maximum, sum and
+// sum e^{s-m}(s-m) (the entropy's) of each row and the row's best columns.
+// Rows are split over column runs and joined by a second, small kernel.
+// All row statistics are fp32, in base 2 (scale and bias carry log2 e).
+//
+// The backward pass recomputes each tile of scores, turns it into G rounded
+// once to the operands' type (bf16: relative 2^-9 of each value; fp16: 2^-11
+// after a power-of-two scale that brings the largest possible |G| of the call
+// to 2^14; fp32: three bf16 planes, 2^-25), and multiplies G with C and X.
+// G is held for a block of rows at a time, sized by a fixed budget.
+// The column sums of dbias use G before the rounding.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "fk_tile_engine.cuh"
+
+namespace fk {
+namespace soft {
+
+using tile::Plan;
+using tile::Unit;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -INFINITY;
+// Below 2^-256 of the maximum a term is zero in fp32; where columns are masked
+// the clamp keeps 0 * -inf out of the entropy sum (a NaN sum stays NaN).
+constexpr float kLowest = -256.f;
+// Columns beyond `top` that the running lists keep: the lists rank by fp32
+// scores, and the final order is settled in fp64 among top + kSpare columns.
+constexpr int kSpare = 2;
+constexpr int kMaxTop = 28;
+// One CTA's 128 rows hold all rows: the second half of a pair's 256-row tile
+// would be empty, and single CTAs spread a short run of columns over all SMs.
+// Otherwise pairs.
+inline int group_of(long long rows) { return rows <= tile::kRows ? 1 : 2; }
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v) { return static_cast<float>(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v) { return static_cast<T>(v); }
+template <>
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+
+// A warp's bias of its half tile's 128 columns, times log2 e, in shared memory;
+// columns past the last count as masked.  `masked`: which of the four
+// 32-column chunks hold a masked column.
+struct BiasTile {
+  static constexpr int kFloats = 128;
+  float *sb;
+  unsigned masked = 0;
+  __device__ __forceinline__ void load(const float *bias, long long col0, long long K, int lane) {
+    __syncwarp();  // the previous tile's values have been read
+    masked = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long col = col0 + i * 32 + lane;
+      const float b = col < K ? __ldg(bias + col) : kNegInf;
+      sb[i * 32 + lane] = b * kLog2e;
+      if (__any_sync(0xffffffffu, b == kNegInf)) masked |= 1u << i;
+    }
+    __syncwarp();
+  }
+};
+
+// The 32 scores of a thread's row in columns [col, col + 32), chunk i of the
+// half tile: in base 2 with a bias, else the products as they are (the scale is
+// positive).  A bias of -inf masks its column whatever the product holds, and
+// columns past the last are masked; returns whether any of the 32 is.
+template <bool BIAS>
+__device__ __forceinline__ bool scores32(const float (&r)[32], float scale2, const BiasTile &bt, int i, long long col,
+                                         long long K, float (&t)[32]) {
+  if (BIAS) {
+    const float4 *sb = reinterpret_cast<const float4 *>(bt.sb + i * 32);
+    const float2 s2 = make_float2(scale2, scale2);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 b = sb[j];
+      const float2 lo = __ffma2_rn(make_float2(r[4 * j], r[4 * j + 1]), s2, make_float2(b.x, b.y));
+      const float2 hi = __ffma2_rn(make_float2(r[4 * j + 2], r[4 * j + 3]), s2, make_float2(b.z, b.w));
+      t[4 * j] = lo.x, t[4 * j + 1] = lo.y, t[4 * j + 2] = hi.x, t[4 * j + 3] = hi.y;
+    }
+    const bool some = bt.masked >> i & 1u;
+    if (some) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (bt.sb[i * 32 + j] == kNegInf) t[j] = kNegInf;
+    }
+    return some;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) t[j] = r[j];
+    const bool some = col + 32 > K;
+    if (some) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (col + j >= K) t[j] = kNegInf;
+    }
+    return some;
+  }
+}
+
+struct RowGrad {  // one row's coefficients
+  float a, l, e, lse2, h;
+  int id;
+  int pad0, pad1;
+};
+
+struct StatArgs {
+  float scale2;
+  const float *bias;  // (B, K) or NULL
+  const int32_t *ids;
+  long long N, K;
+  int parts;  // partial results per row: 2 * runs
+  int L;      // columns kept per partial list, 0: none
+  float4 *part;          // (B, N, parts): m, sum, sum e (t - m), target score
+  float *top_v;          // (B, N, parts, L)
+  int32_t *top_i;
+};
+
+// Joins a row's partial results (one warp per row).
+struct JoinArgs {
+  const float4 *part;
+  const float *top_v;
+  const int32_t *top_i;
+  const int32_t *ids;
+  const void *x, *c;
+  const float *bias;
+  float scale;
+  long long rows, N, K;
+  int d, parts, L, cands, top;  // L: length of a partial list; cands = min(K, top + kSpare)
+  bool vec;  // rows of x and c can be read 16 bytes at a time
+  float *logp, *lse, *entropy, *top_logp;
+  int32_t *top_ids;
+  int *err;
+};
+
+struct Dims {
+  int B;
+  long long N;
+  int K, d, dtype;
+  int planes, pairs, dp;
+  long long Kp;
+};
+
+inline Dims dims_of(const fk_shape &sh) {
+  Dims m;
+  m.B = sh.B, m.N = sh.N, m.K = sh.K, m.d = sh.d, m.dtype = sh.dtype;
+  m.planes = sh.dtype == FK_F32 ? 3 : 1;
+  m.pairs = sh.dtype == FK_F32 ? 6 : 1;
+  m.dp = (sh.d + 7) / 8 * 8;
+  m.Kp = ((long long)sh.K + 63) / 64 * 64;
+  return m;
+}
+
+inline int check_soft(const fk_shape *shape, float scale) {
+  if (!shape) return set_error(FK_EINVAL, "shape is NULL");
+  if (shape->N < 0) return set_error(FK_EINVAL, "N must be >= 0");
+  // the table may be longer than the rows are many
+  const long long n = shape->N > shape->K ? shape->N : shape->K;
+  FK_TRY(check_shape(shape->B, n, shape->K, shape->d, shape->dtype));
+  if (shape->d > (1 << 20)) return set_error(FK_EUNSUPPORTED, "d above 2^20");
+  if (!(scale > 0.f) || !(scale < INFINITY)) return set_error(FK_EINVAL, "scale must be positive and finite");
+  return FK_OK;
+}
+
+inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+// Row tiles x column runs over the workers: the fewest rounds of units, with
+// the start and the partial results of a unit counted as a quarter of a tile.
+inline Plan plan_runs(int B, long long rows, long long cols, int kdim, int pairs, int planes, int row_bytes) {
+  Plan p = {};
+  p.cg = group_of(rows);
+  const int workers = num_sms() / p.cg;
+  p.row_tiles = (int)cdiv(rows, tile::kRows * p.cg);
+  p.col_tiles = (int)cdiv(cols, tile::kCols);
+  p.kblocks = (int)cdiv(kdim, tile::kK);
+  p.pairs = pairs;
+  p.planes = planes;
+  p.ksplits = 1;
+  double best = 1e30;
+  p.runs = 1;
+  for (int runs = 1; runs <= p.col_tiles && runs <= 2 * workers; ++runs) {
+    const double t = (double)cdiv((long long)B * p.row_tiles * runs, workers) * (cdiv(p.col_tiles, runs) + 0.25);
+    if (t < best * 0.999) {
+      best = t;
+      p.runs = runs;
+    }
+  }
+  // rows of one group: 32 MB of the row operand at most, so that they stay in L2
+  const long long g = (32LL << 20) / ((long long)tile::kRows * p.cg * row_bytes);
+  p.group = (int)std::max(1LL, std::min<long long>(g, p.row_tiles));
+  p.units = (int)((long long)B * p.row_tiles * p.runs);
+  return p;
+}
+
+// One tile per unit, the contraction split so that the last round is not
+// mostly idle; a split costs about eight K-blocks (its partial sums).
+inline Plan plan_splits(int B, long long rows, long long cols, long long kdim, int pairs, int planes) {
+  Plan p = {};
+  p.cg = group_of(rows);
+  const int workers = num_sms() / p.cg;
+  p.row_tiles = (int)cdiv(rows, tile::kRows * p.cg);
+  p.col_tiles = (int)cdiv(cols, tile::kCols);
+  p.runs = p.col_tiles;
+  p.kblocks = (int)cdiv(kdim, tile::kK);
+  p.pairs = pairs;
+  p.planes = planes;
+  const long long kt = (long long)p.pairs * p.kblocks;
+  double best = 1e30;
+  p.ksplits = 1;
+  for (int ks = 1; ks <= 16 && ks <= kt; ++ks) {
+    const double t = (double)cdiv((long long)B * p.row_tiles * p.runs * ks, workers) *
+                     ((double)cdiv(kt, ks) + 4.0 + (ks > 1 ? 8.0 : 0.0));
+    if (t < best * 0.98) {
+      best = t;
+      p.ksplits = ks;
+    }
+  }
+  p.group = std::max(1, std::min(p.row_tiles, 16 / p.cg));
+  p.units = (int)((long long)B * p.row_tiles * p.runs * p.ksplits);
+  return p;
+}
+
+inline bool too_many(const Plan &p, int B) {
+  return (double)B * p.row_tiles * p.runs * p.ksplits > 2e9;
+}
+
+template <int kCG, class Epi, bool A_MN, bool B_MN>
+int launch_group(const CUtensorMap &ta, const CUtensorMap &tb, Plan p, const typename Epi::Args &ea, size_t epi_smem,
+                 int ab_fmt, int *err, cudaStream_t s) {
+  auto kern = tile::k_tiles<kCG, A_MN, B_MN, Epi>;
+  constexpr uint32_t stage = tile::Geo<kCG>::kStageBytes;
+  const size_t cap = 227 * 1024 - 1024 - tile::kCtrlBytes;
+  p.stages = (int)std::min<size_t>(tile::kMaxStages, (cap - epi_smem) / stage);
+  
+  p.idesc = sm100::idesc_f32acc((uint32_t)ab_fmt, tile::kRows * kCG, tile::kCols) | (A_MN ? 1u << 15 : 0u) |
+            (B_MN ? 1u << 16 : 0u);
+  const int smem = (int)(1024 + p.stages * stage + tile::kCtrlBytes + epi_smem);
+  FK_TRY(set_smem_limit((const void *)kern, 227 * 1024));
+  const int workers = std::min(num_sms() / kCG, p.units);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(workers * kCG);
+  cfg.blockDim = dim3(tile::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCG > 1 ? 2 : 1;
+  FK_CUDA(cudaLaunchKernelEx(&cfg, kern, ta, tb, p, ea, err));
+  return launched();
+}
+
+template <class Epi, bool A_MN, bool B_MN>
+int launch_tiles(const CUtensorMap &ta, const CUtensorMap &tb, const Plan &p, const typename Epi::Args &ea,
+                 size_t epi_smem, int ab_fmt, int *err, cudaStream_t s) {
+  if (p.cg == 1) return launch_group<1, Epi, A_MN, B_MN>(ta, tb, p, ea, epi_smem, ab_fmt, err, s);
+  return launch_group<2, Epi, A_MN, B_MN>(ta, tb, p, ea, epi_smem, ab_fmt, err, s);
+}
+
+// Tensor map of 16-bit elements: (inner, rows, depth) with the row pitch and
+// depth stride in elements.
+inline int map_16(CUtensorMap *m, const void *base, bool bf16, long long inner, long long rows, long long depth,
+           long long pitch, long long stride, int box_inner, int box_rows) {
+  return encode_tiles(m, base, bf16 ? FK_BF16 : FK_F16, inner, rows, depth, pitch, stride, box_inner, box_rows);
+}
+
+struct Carve {
+  char *base;
+  size_t off = 0;
+  explicit Carve(void *p) : base(static_cast<char *>(p)) {}
+  void *take(size_t bytes) {
+    void *r = base ? base + off : nullptr;
+    off += (bytes + 255) / 256 * 256;
+    return r;
+  }
+};
+
+// Columns a partial list keeps: at least kSpare more than asked for; up to 16
+// in registers (an insertion costs five instructions a place), else 32 in
+// shared memory.
+inline int list_length(int top) { return top == 0 ? 0 : top + kSpare <= 16 ? (top + kSpare + 3) / 4 * 4 : 32; }
+
+struct FwdSpace {
+  Plan p;
+  int L;
+  void *xs, *cs;
+  float4 *part;
+  float *top_v;
+  int32_t *top_i;
+  size_t bytes;
+};
+
+
+// Defined in fk_scores.cu / fk_scores_bias.cu, fk_join.cu and fk_operand.cu.
+int launch_scores(const CUtensorMap &tx, const CUtensorMap &tc, const FwdSpace &f, const StatArgs &a, int fmt, int *err,
+                  cudaStream_t s);
+int launch_scores_bias(const CUtensorMap &tx, const CUtensorMap &tc, const FwdSpace &f, const StatArgs &a, int fmt,
+                       int *err, cudaStream_t s);
+int launch_join(const JoinArgs &j, int dtype, cudaStream_t s);
+int operand(const void *src, int dtype, long long rows, long long rows_per_b, int d, int dp, const RowGrad *g,
+            const float *bias, void *dst, cudaStream_t s);
+
+}  // namespace soft
+}  // namespace fk
