@@ -311,11 +311,11 @@ def _scratch(where: str, workspace, nbytes: int, device, stream):
     if workspace is None:
         if stream is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            return workspace, workspace.data_ptr(), nbytes
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     elif workspace.dtype != torch.uint8 or workspace.dim() != 1:
         raise ValueError(f"{where}: workspace must be a one-dimensional uint8 tensor")
     n = workspace.numel()
@@ -351,15 +351,20 @@ def fk_logprob(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, logp: torch.
     pe = _need(w, "entropy", entropy, f32, row, dev)
     pti = _need(w, "top_ids", top_ids, i32, (B, N, top), dev)
     ptl = _need(w, "top_logp", top_logp, f32, (B, N, top), dev)
+    _call_logprob(shape, dev, (px, pc, pb, scale, pi, pl, ps, pe, top, pti, ptl), workspace, stream)
+    return logp
+
+
+def _call_logprob(shape, dev, args, workspace=None, stream=None) -> None:
+    """lib.fk_logprob on checked arguments."""
+    w = "fk_logprob"
     with _at(dev):
         need = ctypes.c_longlong(0)
-        if st := lib.fk_logprob_workspace(ctypes.byref(shape), top, ctypes.byref(need)):
+        if st := lib.fk_logprob_workspace(ctypes.byref(shape), args[8], ctypes.byref(need)):
             _check(st, w)
         workspace, pw, n = _scratch(w, workspace, need.value, dev, stream)
-        if st := lib.fk_logprob(ctypes.byref(shape), px, pc, pb, scale, pi, pl, ps, pe, top, pti, ptl, pw, n,
-                                _handle(stream, dev)):
+        if st := lib.fk_logprob(ctypes.byref(shape), *args, pw, n, _handle(stream, dev)):
             _check(st, w)
-    return logp
 
 
 def fk_logprob_backward(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, lse: torch.Tensor, entropy=None,
@@ -408,14 +413,20 @@ def fk_moe(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_out: tor
     py, pi = _need(w, "y", y, dt, (T, d), dev), _need(w, "expert_ids", expert_ids, torch.int32, (T, k), dev)
     pg = _need(w, "expert_weights", expert_weights, torch.float32, (T, k), dev)
     shape = FkMoeShape(T, E, d, F, k, _dtype_code(x), act, bool(renormalize))
+    _call_moe(shape, dev, (px, pr, pin, pout, py, pi, pg), workspace, stream)
+    return y
+
+
+def _call_moe(shape, dev, args, workspace=None, stream=None) -> None:
+    """lib.fk_moe on checked arguments."""
+    w = "fk_moe"
     with _at(dev):
         need = ctypes.c_longlong(0)
         if st := lib.fk_moe_workspace(ctypes.byref(shape), ctypes.byref(need)):
             _check(st, w)
         workspace, pw, n = _scratch(w, workspace, need.value, dev, stream)
-        if st := lib.fk_moe(ctypes.byref(shape), px, pr, pin, pout, py, pi, pg, pw, n, _handle(stream, dev)):
+        if st := lib.fk_moe(ctypes.byref(shape), *args, pw, n, _handle(stream, dev)):
             _check(st, w)
-    return y
 
 
 def fk_device_error(stream=None) -> int:

@@ -80,8 +80,8 @@ int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float 
   const FwdSpace f = fwd_space(m, top, workspace);
   const void *xo = x, *co = c;
   if (m.planes == 3) {
-    FK_TRY(operand(x, m.dtype, m.B * m.N, m.N, m.d, m.dp, nullptr, nullptr, f.xs, s));
-    FK_TRY(operand(c, m.dtype, (long long)m.B * m.K, m.K, m.d, m.dp, nullptr, nullptr, f.cs, s));
+    FK_TRY(operand(x, m.dtype, m.B * m.N, m.N, m.d, m.dp, nullptr, f.xs, s));
+    FK_TRY(operand(c, m.dtype, (long long)m.B * m.K, m.K, m.d, m.dp, nullptr, f.cs, s));
     xo = f.xs, co = f.cs;
   }
   const bool bf = m.dtype != FK_F16;

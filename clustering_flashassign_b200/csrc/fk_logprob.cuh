@@ -334,14 +334,50 @@ struct FwdSpace {
 };
 
 
+// One row's operand copy, by a warp: 16-bit rows as they are, fp32 rows as three
+// bf16 planes of dp >= d elements (zero padded).  drop: rows whose gradient is
+// zero whatever they hold (padding), or table rows that a bias of -inf masks,
+// become zero, so that what they hold (NaN included) stays out of the products.
+template <typename T>
+__device__ __forceinline__ void copy_row(const T *src, long long r, long long rows_per_b, int d, int dp, bool drop,
+                                         void *dst, int lane) {
+  const T *in = src + (size_t)r * d;
+  if constexpr (sizeof(T) == 2) {
+    uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(dst) + (size_t)r * d);
+#pragma unroll 4
+    for (int j = lane; j < d / 8; j += 32)
+      out[j] = drop ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(in) + j);
+  } else {
+    const long long b = r / rows_per_b;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(dst) + ((size_t)(b * 3) * rows_per_b + (r - b * rows_per_b)) * dp;
+    const size_t plane = (size_t)rows_per_b * dp;
+    for (int j = 2 * lane; j < dp; j += 64) {
+      float v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) v[i] = j + i < d && !drop ? in[j + i] : 0.f;
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        __nv_bfloat162 h;
+        h.x = __float2bfloat16_rn(v[0]);
+        h.y = __float2bfloat16_rn(v[1]);
+        *reinterpret_cast<__nv_bfloat162 *>(out + p * plane + j) = h;
+        const float2 f = __bfloat1622float2(h);
+        // an infinity (or an overflow of the rounding) leaves no remainder
+        v[0] = fabsf(f.x) < INFINITY ? v[0] - f.x : 0.f;
+        v[1] = fabsf(f.y) < INFINITY ? v[1] - f.y : 0.f;
+      }
+    }
+  }
+}
+
 // Defined in fk_scores.cu / fk_scores_bias.cu, fk_join.cu and fk_operand.cu.
 int launch_scores(const CUtensorMap &tx, const CUtensorMap &tc, const FwdSpace &f, const StatArgs &a, int fmt, int *err,
                   cudaStream_t s);
 int launch_scores_bias(const CUtensorMap &tx, const CUtensorMap &tc, const FwdSpace &f, const StatArgs &a, int fmt,
                        int *err, cudaStream_t s);
 int launch_join(const JoinArgs &j, int dtype, cudaStream_t s);
-int operand(const void *src, int dtype, long long rows, long long rows_per_b, int d, int dp, const RowGrad *g,
-            const float *bias, void *dst, cudaStream_t s);
+int operand(const void *src, int dtype, long long rows, long long rows_per_b, int d, int dp, const float *bias,
+            void *dst, cudaStream_t s);
 
 }  // namespace soft
 }  // namespace fk

@@ -6,34 +6,37 @@ namespace soft {
 namespace {
 
 // ------------------------------------------------------------------ backward
-// Coefficients of every row, and the largest bound of |G| over the rows (float
-// bits; positive floats order as integers).
+// Coefficients of every row (a warp each), its copy for the products (see
+// fk_operand.cu: a row without any gradient becomes zero), and the largest
+// bound of |G| over the rows (float bits; positive floats order as integers).
+template <typename T>
 __global__ void __launch_bounds__(256)
-    k_row_grads(const int32_t *ids, const float *lse, const float *entropy, const float *dlogp, const float *dlse,
-                const float *dent, long long rows, int K, RowGrad *out, unsigned *bound, int *err) {
+    k_rows(const int32_t *ids, const float *lse, const float *entropy, const float *dlogp, const float *dlse,
+           const float *dent, long long rows, long long rows_per_b, int K, RowGrad *out, unsigned *bound, const T *x,
+           int d, int dp, void *xs, int *err) {
   pdl_wait();
-  const long long r = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  float big = 0.f;
-  if (r < rows) {
-    RowGrad g = {};
-    g.id = ids[r];
-    if (g.id >= K) atomicCAS(err, DEV_OK, DEV_BAD_ID);
-    if (g.id < 0 || g.id >= K) g.id = -1;
-    g.a = dlogp && g.id >= 0 ? dlogp[r] : 0.f;
-    g.l = dlse ? dlse[r] : 0.f;
-    g.e = dent ? dent[r] : 0.f;
-    g.h = dent ? entropy[r] : 0.f;
-    const float v = lse[r];
-    g.lse2 = v * kLog2e;
-    if (v == kNegInf) g.a = g.l = g.e = 0.f;  // every column is masked
-    if (g.a == 0.f && g.l == 0.f && g.e == 0.f) g.id = -2;  // G is zero whatever the scores hold
+  const int lane = threadIdx.x & 31;
+  const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  RowGrad g = {};
+  g.id = ids[r];
+  if (g.id >= K && lane == 0) atomicCAS(err, DEV_OK, DEV_BAD_ID);
+  if (g.id < 0 || g.id >= K) g.id = -1;
+  g.a = dlogp && g.id >= 0 ? dlogp[r] : 0.f;
+  g.l = dlse ? dlse[r] : 0.f;
+  g.e = dent ? dent[r] : 0.f;
+  g.h = dent ? entropy[r] : 0.f;
+  const float v = lse[r];
+  g.lse2 = v * kLog2e;
+  if (v == kNegInf) g.a = g.l = g.e = 0.f;  // every column is masked
+  if (g.a == 0.f && g.l == 0.f && g.e == 0.f) g.id = -2;  // G is zero whatever the scores hold
+  if (lane == 0) {
     out[r] = g;
     // |p (log p + H)| <= max(1 / e, log K) <= log K + 1
-    big = fabsf(g.a) + fabsf(g.l) + fabsf(g.e) * (logf((float)K) + 1.f);
+    const float big = fabsf(g.a) + fabsf(g.l) + fabsf(g.e) * (logf((float)K) + 1.f);
+    if (bound && big > 0.f) atomicMax(bound, __float_as_uint(big));
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-  if ((threadIdx.x & 31) == 0 && big > 0.f) atomicMax(bound, __float_as_uint(big));
+  copy_row<T>(x, r, rows_per_b, d, dp, g.id == -2, xs, lane);
 }
 
 // The power of two that brings `bound` to [2^13, 2^14), within [2^-100, 2^100].
@@ -94,26 +97,25 @@ struct GradEpi {
   __device__ __forceinline__ void chunk(const float (&acc)[32], long long col, int i) {
     {
       float v[32];
-      scores32<BIAS>(acc, a.scale2, bt, i, col, a.K, v);
+      const bool some_masked = scores32<BIAS>(acc, a.scale2, bt, i, col, a.K, v);
+      // y = p (l - a - e (log p + H)) = p (c1 + c2 log2 p)
       const float2 nl = make_float2(-q.lse2, -q.lse2), sc = make_float2(a.scale2, a.scale2);
-      const bool full = __any_sync(0xffffffffu, q.e != 0.f || q.id == -2);
-      if (!full) {  // y = p (l - a)
-        const float2 c2 = make_float2(q.l - q.a, q.l - q.a);
+      const float2 c1 = make_float2(q.l - q.a - q.e * q.h, q.l - q.a - q.e * q.h);
+      const float2 c2 = make_float2(-q.e * kLn2, -q.e * kLn2);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 w = make_float2(v[2 * j], v[2 * j + 1]);
-          const float2 lp2 = BIAS ? __fadd2_rn(w, nl) : __ffma2_rn(w, sc, nl);
-          const float2 y = __fmul2_rn(make_float2(ex2(lp2.x), ex2(lp2.y)), c2);
-          v[2 * j] = y.x;
-          v[2 * j + 1] = y.y;
-        }
-      } else {  // entropy terms, or rows without any gradient among the 32
+      for (int j = 0; j < 16; ++j) {
+        const float2 w = make_float2(v[2 * j], v[2 * j + 1]);
+        float2 lp2 = BIAS ? __fadd2_rn(w, nl) : __ffma2_rn(w, sc, nl);
+        const float2 p = make_float2(ex2(lp2.x), ex2(lp2.y));
+        if (some_masked) lp2 = make_float2(fmaxf(lp2.x, kLowest), fmaxf(lp2.y, kLowest));
+        const float2 y = __fmul2_rn(p, __ffma2_rn(lp2, c2, c1));
+        v[2 * j] = y.x;
+        v[2 * j + 1] = y.y;
+      }
+      if (__any_sync(0xffffffffu, q.id == -2)) {  // rows without any gradient among the 32
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float lp2 = BIAS ? v[j] - q.lse2 : fmaf(v[j], a.scale2, -q.lse2);
-          const float y = ex2(lp2) * (q.l - q.a - q.e * fmaf(fmaxf(lp2, kLowest), kLn2, q.h));
-          v[j] = q.id == -2 ? 0.f : y;
-        }
+        for (int j = 0; j < 32; ++j)
+          if (q.id == -2) v[j] = 0.f;
       }
       const unsigned rel = (unsigned)(q.id - (int)col);
       if (__any_sync(0xffffffffu, rel < 32u)) {  // the target's own term, unless it is masked
@@ -244,19 +246,28 @@ struct StoreEpi {
   __device__ void end(const Unit &) {}
 };
 
-// out = the sum of the parts, in order.
-template <typename T>
+// out = the sum of the parts, in order; four columns a thread where rows allow it.
+template <typename T, int V>
 __global__ void __launch_bounds__(256)
-    k_sum_parts(const float *part, int parts, long long slot, long long rows, long long cols, long long rows_per_b,
-                T *out, long long pitch, long long batch_stride) {
+    k_sum_parts(const float *part, int parts, long long slot, long long n, T *out) {
   pdl_wait();
-  const long long n = rows * cols;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
-    float s = 0.f;
-    for (int p = 0; p < parts; ++p) s += part[p * slot + i];
-    const long long row = i / cols, b = row / rows_per_b;
-    out[b * batch_stride + (row - b * rows_per_b) * pitch + (i - row * cols)] = from_f<T>(s);
+  const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * V;
+  if (i >= n) return;
+  float s[V] = {};
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    float v[V];
+    if constexpr (V == 4) *reinterpret_cast<float4 *>(v) = __ldcs(reinterpret_cast<const float4 *>(part + p * slot + i));
+    else v[0] = part[p * slot + i];
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] += v[j];
   }
+  T h[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) h[j] = from_f<T>(s[j]);
+  if constexpr (V == 4 && sizeof(T) == 2) *reinterpret_cast<uint2 *>(out + i) = *reinterpret_cast<uint2 *>(h);
+  else if constexpr (V == 4) *reinterpret_cast<float4 *>(out + i) = *reinterpret_cast<float4 *>(h);
+  else out[i] = h[0];
 }
 
 // dbias[b][k] (+)= the sum of the row blocks' column sums, in a fixed order.
@@ -315,13 +326,15 @@ BwdSpace bwd_space(const Dims &m, bool bias, bool dbias, void *base) {
   return f;
 }
 
+// Partial sums of (B, rows, d) values, contiguous like the result.
 template <typename T>
-int launch_sum_parts(const float *part, const Plan &p, int B, long long rows, long long cols, void *out,
-                     long long pitch, long long batch_stride, cudaStream_t s) {
-  const long long n = (long long)B * rows * cols;
-  const long long blocks = std::min<long long>(cdiv(n, 256), (long long)num_sms() * 16);
-  FK_CUDA(launch_pdl(k_sum_parts<T>, dim3((unsigned)blocks), dim3(256), 0, s, part, p.ksplits, n, (long long)B * rows,
-                     cols, rows, static_cast<T *>(out), pitch, batch_stride));
+int launch_sum_parts(const float *part, int parts, long long n, int d, void *out, cudaStream_t s) {
+  T *o = static_cast<T *>(out);
+  if (d % 4 == 0) {
+    FK_CUDA(launch_pdl(k_sum_parts<T, 4>, dim3((unsigned)cdiv(n, 1024)), dim3(256), 0, s, part, parts, n, n, o));
+  } else {
+    FK_CUDA(launch_pdl(k_sum_parts<T, 1>, dim3((unsigned)cdiv(n, 256)), dim3(256), 0, s, part, parts, n, n, o));
+  }
   return launched();
 }
 
@@ -391,7 +404,7 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
         sa.slot = (long long)bn * nr * m.d;
         FK_TRY((launch_tiles<StoreEpi<T, sizeof(T) == 4>, false, true>(tg, tcm, px, sa, 0, fmt, err, s)));
         if (sa.part)
-          FK_TRY(launch_sum_parts<T>(f.partx, px, bn, nr, m.d, sa.out, m.d, sa.batch_stride, s));
+          FK_TRY(launch_sum_parts<T>(f.partx, px.ksplits, sa.slot, m.d, sa.out, s));
       }
       // dc = G^T X: the contraction is the rows
       if (dc) {
@@ -418,9 +431,7 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
         sa.add = r0 > 0;
         FK_TRY((launch_tiles<StoreEpi<T, sizeof(T) == 4>, true, true>(tg, txm, pw, sa, 0, fmt, err, s)));
         if (sa.part && r0 + nr >= m.N) {
-          Plan all = f.pw;
-          all.ksplits = f.nr < m.N ? f.pw.ksplits : pw.ksplits;
-          FK_TRY(launch_sum_parts<T>(f.partw, all, bn, m.K, m.d, sa.out, m.d, sa.batch_stride, s));
+          FK_TRY(launch_sum_parts<T>(f.partw, f.nr < m.N ? f.pw.ksplits : pw.ksplits, sa.slot, m.d, sa.out, s));
         }
       }
     }
@@ -502,13 +513,17 @@ int fk_logprob_backward(const fk_shape *shape, const void *x, const void *c, con
   FK_TRY(soft_error_word(&err));
   const BwdSpace f = bwd_space(m, bias != nullptr, dbias != nullptr, workspace);
   const long long rows = m.B * m.N;
-  FK_CUDA(cudaMemsetAsync(f.bound, 0, 16, s));
-  k_row_grads<<<(unsigned)cdiv(rows, 256), 256, 0, s>>>(ids, lse, entropy, dlogp, dlse, dentropy, rows, m.K, f.rows,
-                                                        f.bound, err);
-  FK_TRY(launched());
-  FK_CUDA(cudaGetLastError());
-  FK_TRY(operand(x, m.dtype, rows, m.N, m.d, m.dp, f.rows, nullptr, f.xs, s));
-  if (f.cs) FK_TRY(operand(c, m.dtype, (long long)m.B * m.K, m.K, m.d, m.dp, nullptr, bias, f.cs, s));
+  unsigned *bound = m.dtype == FK_F16 ? f.bound : nullptr;  // fp16 alone needs G scaled
+  if (bound) FK_CUDA(cudaMemsetAsync(bound, 0, 16, s));
+  auto prepare = [&](auto tag) -> int {
+    using T = decltype(tag);
+    FK_CUDA(launch_pdl(k_rows<T>, dim3((unsigned)cdiv(rows, 8)), dim3(256), 0, s, ids, lse, entropy, dlogp, dlse,
+                       dentropy, rows, m.N, m.K, f.rows, bound, static_cast<const T *>(x), m.d, m.dp, f.xs, err));
+    return launched();
+  };
+  if (m.dtype == FK_F32) FK_TRY(prepare(float{}));
+  else FK_TRY(prepare(__half{}));  // 16-bit rows are copied as bits
+  if (f.cs) FK_TRY(operand(c, m.dtype, (long long)m.B * m.K, m.K, m.d, m.dp, bias, f.cs, s));
   // a dropped row's or column's scores do not count (its G is zero), so the
   // recomputed scores may read the cleaned copies as well
   const void *co = f.cs ? f.cs : c;

@@ -22,7 +22,8 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import FK_ACT_GELU, FK_ACT_SILU, fk_logprob, fk_logprob_backward, fk_moe
+from . import (DTYPES, FK_ACT_GELU, FK_ACT_SILU, FkMoeShape, FkShape, _call_logprob, _call_moe,
+               fk_logprob_backward)
 
 
 class TokenLogProbs(NamedTuple):
@@ -34,13 +35,24 @@ class TokenLogProbs(NamedTuple):
 
 
 def _forward(x, c, bias, ids, scale, top):
-    rows, dev = ids.shape, x.device
-    logp, lse, entropy = (torch.empty(rows, dtype=torch.float32, device=dev) for _ in range(3))
-    top_ids = top_logp = None
+    (B, N, d), K, dev = x.shape, c.shape[1], x.device
+    if not x.is_cuda or x.dtype not in DTYPES:
+        raise ValueError(f"x must be an fp16, bf16 or fp32 CUDA tensor, got {x.dtype} on {dev}")
+    if c.dtype != x.dtype or c.shape != (B, K, d) or c.device != dev or ids.device != dev:
+        raise ValueError(f"c must be {x.dtype}, of {B} tables of width {d}, and like ids on {dev}: got {c.dtype} of "
+                         f"shape {tuple(c.shape)} on {c.device}, ids on {ids.device}")
+    if bias is not None and (bias.shape != (B, K) or bias.device != dev):
+        raise ValueError(f"bias must be of shape {(B, K)} on {dev}: got {tuple(bias.shape)} on {bias.device}")
+    logp = x.new_empty((B, N), dtype=torch.float32)
+    lse, entropy = torch.empty_like(logp), torch.empty_like(logp)
+    top_ids = top_logp = pi = pl = None
     if top:
-        top_ids = torch.empty((*rows, top), dtype=torch.int32, device=dev)
-        top_logp = torch.empty((*rows, top), dtype=torch.float32, device=dev)
-    fk_logprob(x, c, ids, logp, lse, entropy, top_ids, top_logp, bias, scale)
+        top_ids = x.new_empty((B, N, top), dtype=torch.int32)
+        top_logp = x.new_empty((B, N, top), dtype=torch.float32)
+        pi, pl = top_ids.data_ptr(), top_logp.data_ptr()
+    _call_logprob(FkShape(B, N, K, d, DTYPES[x.dtype]), dev,
+                  (x.data_ptr(), c.data_ptr(), None if bias is None else bias.data_ptr(), scale, ids.data_ptr(),
+                   logp.data_ptr(), lse.data_ptr(), entropy.data_ptr(), top, pi, pl))
     return logp, lse, entropy, top_ids, top_logp
 
 
@@ -135,18 +147,29 @@ def expert_mixture(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_
     """
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
-    if torch.is_grad_enabled() and any(t.requires_grad for t in (x, router, w_in, w_out)):
+    if torch.is_grad_enabled() and (x.requires_grad or router.requires_grad or w_in.requires_grad
+                                    or w_out.requires_grad):
         raise RuntimeError("expert_mixture has no backward pass: call it under torch.no_grad()")
-    if x.dim() < 1:
-        raise ValueError("x must be (..., d)")
-    k, lead, dev = int(top_k), x.shape[:-1], x.device
+    if x.dim() < 1 or router.dim() != 2 or w_in.dim() != 3 or w_out.dim() != 3:
+        raise ValueError("x must be (..., d), router (E, d), w_in (E, 2F, d), w_out (E, d, F)")
+    k, d, (E, _, F), dt, dev = int(top_k), x.shape[-1], w_out.shape, x.dtype, x.device
+    if not x.is_cuda or dt not in DTYPES:
+        raise ValueError(f"x must be an fp16 or bf16 CUDA tensor, got {dt} on {dev}")
+    for name, t, shape in (("router", router, (E, d)), ("w_in", w_in, (E, 2 * F, d)), ("w_out", w_out, (E, d, F))):
+        if t.dtype != dt or t.shape != shape or t.device != dev:
+            raise ValueError(f"{name} must be {dt} of shape {shape} on {dev}, got {t.dtype} of shape "
+                             f"{tuple(t.shape)} on {t.device}")
     flat = x.dim() == 2
-    xs = (x if flat else x.reshape(-1, x.shape[-1])).contiguous()
+    xs = (x if flat else x.reshape(-1, d)).contiguous()
+    router, w_in, w_out = router.contiguous(), w_in.contiguous(), w_out.contiguous()
+    T = xs.shape[0]
     y = torch.empty_like(xs)
-    ids = torch.empty((xs.shape[0], k), dtype=torch.int32, device=dev)
-    weights = torch.empty((xs.shape[0], k), dtype=torch.float32, device=dev)
-    fk_moe(xs, router.contiguous(), w_in.contiguous(), w_out.contiguous(), y, ids, weights, _ACTIVATIONS[activation],
-           renormalize)
+    ids = xs.new_empty((T, k), dtype=torch.int32)
+    weights = xs.new_empty((T, k), dtype=torch.float32)
+    _call_moe(FkMoeShape(T, E, d, F, k, DTYPES[dt], _ACTIVATIONS[activation], bool(renormalize)), dev,
+              (xs.data_ptr(), router.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), y.data_ptr(), ids.data_ptr(),
+               weights.data_ptr()))
     if flat:
         return ExpertMixture(y, ids, weights)
+    lead = x.shape[:-1]
     return ExpertMixture(y.reshape(x.shape), ids.reshape(lead + (k,)), weights.reshape(lead + (k,)))
