@@ -49,10 +49,15 @@ constexpr float kLowest = -256.f;
 // scores, and the final order is settled in fp64 among top + kSpare columns.
 constexpr int kSpare = 2;
 constexpr int kMaxTop = 28;
-// One CTA's 128 rows hold all rows: the second half of a pair's 256-row tile
-// would be empty, and single CTAs spread a short run of columns over all SMs.
-// Otherwise pairs.
-inline int group_of(long long rows) { return rows <= tile::kRows ? 1 : 2; }
+inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+// CTAs per tile.  Pairs halve the operand traffic per product, which counts when
+// the tensor cores are busy: with two rounds of 128 x 256 tiles of some depth
+// for all SMs, and more rows than one CTA holds.  Less work is spread over
+// single CTAs (N 512, K 1000, d 256: scores 9.1 us against 10.6, dX 11.3
+// against 14.4, dC 11.0 against 13.1; dX at N 1777, K 20003, d 1024, 56 deep
+// tiles: 69 us against 63 by pairs).
+inline int group_of(long long rows, double tiles) { return rows <= tile::kRows || tiles < 2.0 * num_sms() ? 1 : 2; }
 
 __device__ __forceinline__ float ex2(float v) {
   float r;
@@ -200,13 +205,12 @@ inline int check_soft(const fk_shape *shape, float scale) {
   return FK_OK;
 }
 
-inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
 // Row tiles x column runs over the workers: the fewest rounds of units, with
 // the start and the partial results of a unit counted as a quarter of a tile.
 inline Plan plan_runs(int B, long long rows, long long cols, int kdim, int pairs, int planes, int row_bytes) {
   Plan p = {};
-  p.cg = group_of(rows);
+  p.cg = group_of(rows, (double)B * cdiv(rows, tile::kRows) * cdiv(cols, tile::kCols));
   const int workers = num_sms() / p.cg;
   p.row_tiles = (int)cdiv(rows, tile::kRows * p.cg);
   p.col_tiles = (int)cdiv(cols, tile::kCols);
@@ -234,7 +238,8 @@ inline Plan plan_runs(int B, long long rows, long long cols, int kdim, int pairs
 // mostly idle; a split costs about eight K-blocks (its partial sums).
 inline Plan plan_splits(int B, long long rows, long long cols, long long kdim, int pairs, int planes) {
   Plan p = {};
-  p.cg = group_of(rows);
+  const double depth = std::max(1.0, pairs * cdiv(kdim, tile::kK) / 16.0);
+  p.cg = group_of(rows, (double)B * cdiv(rows, tile::kRows) * cdiv(cols, tile::kCols) * depth);
   const int workers = num_sms() / p.cg;
   p.row_tiles = (int)cdiv(rows, tile::kRows * p.cg);
   p.col_tiles = (int)cdiv(cols, tile::kCols);

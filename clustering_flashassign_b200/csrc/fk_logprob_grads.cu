@@ -330,7 +330,7 @@ BwdSpace bwd_space(const Dims &m, bool bias, bool dbias, void *base) {
 template <typename T>
 int launch_sum_parts(const float *part, int parts, long long n, int d, void *out, cudaStream_t s) {
   T *o = static_cast<T *>(out);
-  if (d % 4 == 0) {
+  if (d % 4 == 0 && n >= 1 << 20) {  // fewer values: one a thread keeps more loads in flight
     FK_CUDA(launch_pdl(k_sum_parts<T, 4>, dim3((unsigned)cdiv(n, 1024)), dim3(256), 0, s, part, parts, n, n, o));
   } else {
     FK_CUDA(launch_pdl(k_sum_parts<T, 1>, dim3((unsigned)cdiv(n, 256)), dim3(256), 0, s, part, parts, n, n, o));
