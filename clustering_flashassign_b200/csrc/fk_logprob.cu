@@ -10,7 +10,8 @@ FwdSpace fwd_space(const Dims &m, int top, void *base) {
   f.p = plan_runs(m.B, m.N, m.K, m.d, m.pairs, m.planes, m.dp * 2 * m.planes);
   f.L = list_length(top);
   Carve w(base);
-  const long long parts = 2LL * f.p.runs;
+  const bool seg = f.p.kblocks * f.p.pairs > tile::kSegBlocks;
+  const long long parts = f.parts = stat_warps(seg, f.L) / 4 * f.p.runs;
   f.part = (float4 *)w.take((size_t)m.B * m.N * parts * sizeof(float4));
   if (f.L) {
     f.top_v = (float *)w.take((size_t)m.B * m.N * parts * f.L * 4);
@@ -94,7 +95,7 @@ int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float 
   a.bias = bias;
   a.ids = ids;
   a.N = m.N, a.K = m.K;
-  a.parts = 2 * f.p.runs;
+  a.parts = f.parts;
   a.L = f.L;
   a.part = f.part, a.top_v = f.top_v, a.top_i = f.top_i;
   FK_TRY((bias ? launch_scores_bias : launch_scores)(tx, tc, f, a, bf ? 1 : 0, err, s));

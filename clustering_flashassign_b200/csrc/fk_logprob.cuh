@@ -83,19 +83,19 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
-// A warp's bias of its half tile's 128 columns, times log2 e, in shared memory;
-// columns past the last count as masked.  `masked`: which of the four
-// 32-column chunks hold a masked column.
+// A warp's bias of its (at most four) 32-column chunks of a tile, times log2 e,
+// in shared memory; columns past the last count as masked.  `masked`: which of
+// the chunks hold a masked column.
 struct BiasTile {
   static constexpr int kFloats = 128;
   float *sb;
   unsigned masked = 0;
-  __device__ __forceinline__ void load(const float *bias, long long col0, long long K, int lane) {
+  __device__ __forceinline__ void load(const float *bias, long long col0, int stride, long long K, int lane) {
     __syncwarp();  // the previous tile's values have been read
     masked = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const long long col = col0 + i * 32 + lane;
+      const long long col = col0 + i * stride + lane;
       const float b = col < K ? __ldg(bias + col) : kNegInf;
       sb[i * 32 + lane] = b * kLog2e;
       if (__any_sync(0xffffffffu, b == kNegInf)) masked |= 1u << i;
@@ -104,8 +104,8 @@ struct BiasTile {
   }
 };
 
-// The 32 scores of a thread's row in columns [col, col + 32), chunk i of the
-// half tile: in base 2 with a bias, else the products as they are (the scale is
+// The 32 scores of a thread's row in columns [col, col + 32), the warp's
+// chunk i: in base 2 with a bias, else the products as they are (the scale is
 // positive).  A bias of -inf masks its column whatever the product holds, and
 // columns past the last are masked; returns whether any of the 32 is.
 template <bool BIAS>
@@ -152,7 +152,7 @@ struct StatArgs {
   const float *bias;  // (B, K) or NULL
   const int32_t *ids;
   long long N, K;
-  int parts;  // partial results per row: 2 * runs
+  int parts;  // partial results per row: 2 or 3 * runs
   int L;      // columns kept per partial list, 0: none
   float4 *part;          // (B, N, parts): m, sum, sum e (t - m), target score
   float *top_v;          // (B, N, parts, L)
@@ -282,7 +282,7 @@ int launch_group(const CUtensorMap &ta, const CUtensorMap &tb, Plan p, const typ
   const int workers = std::min(num_sms() / kCG, p.units);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(workers * kCG);
-  cfg.blockDim = dim3(tile::kThreads);
+  cfg.blockDim = dim3(tile::Shape<Epi>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -326,11 +326,16 @@ struct Carve {
 // Columns a partial list keeps: at least kSpare more than asked for; up to 16
 // in registers (an insertion costs five instructions a place), else 32 in
 // shared memory.
-inline int list_length(int top) { return top == 0 ? 0 : top + kSpare <= 16 ? (top + kSpare + 3) / 4 * 4 : 32; }
+constexpr int list_length(int top) { return top == 0 ? 0 : top + kSpare <= 16 ? (top + kSpare + 3) / 4 * 4 : 32; }
+
+// Epilogue warps of the score kernels.  Where the contraction is short the
+// epilogue's latency is the limit and a third warp per quadrant hides more of it;
+// longer lists and summed segments need the registers instead.
+constexpr int stat_warps(bool seg, int L) { return !seg && L <= 8 ? 12 : 8; }
 
 struct FwdSpace {
   Plan p;
-  int L;
+  int L, parts;
   void *xs, *cs;
   float4 *part;
   float *top_v;

@@ -64,6 +64,7 @@ template <typename T, bool BIAS, bool SEG>
 struct GradEpi {
   using Args = GradArgs;
   static constexpr bool kSeg = SEG;
+  static constexpr int kWarps = 8;
   const Args &a;
   const int r, lane;
   BiasTile bt;
@@ -89,9 +90,9 @@ struct GradEpi {
     const long long blk = (row0 + (r & ~31)) >> 5;
     cp = a.colpart && blk < a.nblk ? a.colpart + (w.b * a.nblk + blk) * a.Kp : nullptr;
   }
-  static size_t smem_bytes() { return BIAS ? tile::kEpiWarps * BiasTile::kFloats * 4 : 0; }
-  __device__ __forceinline__ void prepare(long long col0) {
-    if (BIAS) bt.load(bias, col0, a.K, lane);
+  static size_t smem_bytes() { return BIAS ? kWarps * BiasTile::kFloats * 4 : 0; }
+  __device__ __forceinline__ void prepare(long long col0, int stride) {
+    if (BIAS) bt.load(bias, col0, stride, a.K, lane);
   }
   __device__ __forceinline__ bool skip(long long col) const { return col >= a.Kp; }
   __device__ __forceinline__ void chunk(const float (&acc)[32], long long col, int i) {
@@ -201,6 +202,7 @@ template <typename T, bool SEG>
 struct StoreEpi {
   using Args = StoreArgs;
   static constexpr bool kSeg = SEG;
+  static constexpr int kWarps = 8;
   const Args &a;
   const int r;
   float alpha;
@@ -220,7 +222,7 @@ struct StoreEpi {
     out = static_cast<T *>(a.out) + w.b * a.batch_stride + row * a.pitch;
     if (a.part) part = a.part + w.ks * a.slot + (w.b * a.rows + row) * a.cols;
   }
-  __device__ __forceinline__ void prepare(long long) {}
+  __device__ __forceinline__ void prepare(long long, int) {}
   __device__ __forceinline__ bool skip(long long col) const { return col >= a.cols; }
   __device__ __forceinline__ void chunk(const float (&acc)[32], long long col, int) {
     if (row >= a.rows) return;
