@@ -17,6 +17,10 @@ __device__ __forceinline__ void join_stats(float &m, float &s, float &u, float m
   m = mm;
 }
 
+// Rounding must not make a log probability positive or an entropy negative.
+// (NaN stays.)
+__device__ __forceinline__ float at_least_0(float v) { return v < 0.f ? 0.f : v; }
+
 // Scores of C columns in fp64, by LPR lanes, from the operands as given:
 // products of 16-bit values are exact, and fp64 sums keep neighbours in rank
 // apart that the fp32 accumulation cannot.
@@ -156,8 +160,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
     const bool valid = id >= 0 && id < a.K;
     if (id >= a.K) atomicCAS(a.err, DEV_OK, DEV_BAD_ID);
     a.lse[r] = none ? kNegInf : (m + ls) * kLn2;
-    if (a.entropy) a.entropy[r] = none ? 0.f : (ls - u / s) * kLn2;
-    a.logp[r] = !valid ? 0.f : (none || (tgt == kNegInf && s == s)) ? kNegInf : ((tgt - m) - ls) * kLn2;
+    if (a.entropy) a.entropy[r] = none ? 0.f : at_least_0((ls - u / s) * kLn2);
+    a.logp[r] = !valid ? 0.f : (none || (tgt == kNegInf && s == s)) ? kNegInf : -at_least_0((ls - (tgt - m)) * kLn2);
   }
   if (a.top == 0) return;
 
@@ -289,9 +293,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
   }
   if (live && lane < a.cands && rank < a.top) {
     a.top_ids[r * a.top + rank] = mine;
-    a.top_logp[r * a.top + rank] = v == (double)kNegInf && s == s ? kNegInf
-                                                                  : (float)(v - (double)(none ? kNegInf : m) * M_LN2) -
-                                                                        ls * kLn2;
+    const float lp = (float)(v - (double)(none ? kNegInf : m) * M_LN2) - ls * kLn2;
+    a.top_logp[r * a.top + rank] = v == (double)kNegInf && s == s ? kNegInf : -at_least_0(-lp);
   }
 }
 

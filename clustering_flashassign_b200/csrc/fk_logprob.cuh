@@ -200,6 +200,8 @@ inline int check_soft(const fk_shape *shape, float scale) {
   // the table may be longer than the rows are many
   const long long n = shape->N > shape->K ? shape->N : shape->K;
   FK_TRY(check_shape(shape->B, n, shape->K, shape->d, shape->dtype));
+  // row numbers of the last tile's empty rows are ints too
+  if (shape->N > 0x7fffffffLL - 512) return set_error(FK_EUNSUPPORTED, "N above 2^31 - 513");
   if (shape->d > (1 << 20)) return set_error(FK_EUNSUPPORTED, "d above 2^20");
   if (!(scale > 0.f) || !(scale < INFINITY)) return set_error(FK_EINVAL, "scale must be positive and finite");
   return FK_OK;

@@ -309,7 +309,7 @@ constexpr long long kGradBudget = 4LL << 30;  // bytes of G held at a time
 BwdSpace bwd_space(const Dims &m, bool bias, bool dbias, void *base) {
   BwdSpace f = {};
   const long long row_bytes = m.Kp * 2 * m.planes;
-  f.nr = std::min<long long>(m.N, std::max<long long>(256, kGradBudget / row_bytes / 256 * 256));
+  f.nr = std::min<long long>(std::max<long long>(m.N, 1), std::max<long long>(256, kGradBudget / row_bytes / 256 * 256));
   f.bn = f.nr < m.N ? 1 : (int)std::max<long long>(1, std::min<long long>(m.B, kGradBudget / (row_bytes * f.nr)));
   f.pg = plan_runs(f.bn, f.nr, m.Kp, m.d, m.pairs, m.planes, m.dp * 2 * m.planes);
   f.px = plan_splits(f.bn, f.nr, m.d, m.K, m.pairs, m.planes);
@@ -479,27 +479,25 @@ int fk_logprob_backward(const fk_shape *shape, const void *x, const void *c, con
   const Dims m = dims_of(*shape);
   const bool al = m.dtype != FK_F32;
   FK_TRY(check_ptr(c, "c", al));
-  if (dc) {
-    FK_TRY(check_ptr(dc, "dc", true));
-    FK_TRY(check_dev(dc, "dc"));
+  if (dc) FK_TRY(check_ptr(dc, "dc", true));
+  if (m.N > 0) {
+    FK_TRY(check_ptr(x, "x", al));
+    FK_TRY(check_ptr(ids, "ids", false));
+    FK_TRY(check_ptr(lse, "lse", false));
+    if (dentropy) FK_TRY(check_ptr(entropy, "entropy", false));
+    if (dx) FK_TRY(check_ptr(dx, "dx", true));
+    FK_TRY(check_ptr(workspace, "workspace", true));
+    if (workspace_bytes < need)
+      return set_error(FK_EINVAL, "workspace is smaller than fk_logprob_backward_workspace asks for");
   }
+  FK_TRY(check_dev_opt(dc, "dc"));
   FK_TRY(check_dev_opt(dbias, "dbias"));
   if (m.N == 0) {  // no rows: the table's gradients are zero
     if (dc) FK_CUDA(cudaMemsetAsync(dc, 0, (size_t)m.B * m.K * m.d * esize(m.dtype), s));
     if (dbias) FK_CUDA(cudaMemsetAsync(dbias, 0, (size_t)m.B * m.K * 4, s));
     return FK_OK;
   }
-  FK_TRY(check_ptr(x, "x", al));
-  FK_TRY(check_ptr(ids, "ids", false));
-  FK_TRY(check_ptr(lse, "lse", false));
-  if (dentropy) FK_TRY(check_ptr(entropy, "entropy", false));
-  if (dx) {
-    FK_TRY(check_ptr(dx, "dx", true));
-    FK_TRY(check_dev(dx, "dx"));
-  }
-  FK_TRY(check_ptr(workspace, "workspace", true));
-  if (workspace_bytes < need)
-    return set_error(FK_EINVAL, "workspace is smaller than fk_logprob_backward_workspace asks for");
+  FK_TRY(check_dev_opt(dx, "dx"));
   FK_TRY(check_dev(x, "x"));
   FK_TRY(check_dev(c, "c"));
   FK_TRY(check_dev_opt(bias, "bias"));

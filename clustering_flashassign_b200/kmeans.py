@@ -71,6 +71,7 @@ class FlashKMeans:
     FlashKMeans(d, k, niter=20, tol=0.0, dtype=torch.float16, device=None, seed=0)
       train(data)        fit on data (N, d) or (B, N, d); sets self.centroids
       predict(data)      ids against the trained centroids (fk_assign)
+      log_prob(data)     soft assignment to the trained centroids (fk_logprob)
       fit_predict(data)  train, then the ids of the last assignment
     device None: the current CUDA device.  When a torch.distributed process group
     is initialised, every rank passes its own contiguous block of the points (the
@@ -132,6 +133,28 @@ class FlashKMeans:
         ids = torch.empty(x.shape[:2], dtype=torch.int32, device=self.device)
         fk_assign(x, c.to(self.dtype).contiguous(), ids)
         return ids[0] if squeeze else ids
+
+    def log_prob(self, data: torch.Tensor, ids: torch.Tensor | None = None, temperature: float = 1.0,
+                 top: int = 0):
+        """Soft assignment: log probabilities under softmax_k(-|x - c_k|^2 / temperature) of the
+        trained centroids.  ids: the clusters asked for (default: the nearest one, predict()).
+        Returns soft.TokenLogProbs: logp of ids, entropy of the assignment, the `top` likeliest
+        clusters; lse omits -|x|^2 / temperature, which all clusters of a row share."""
+        from .soft import token_log_probs
+        if self.centroids is None:
+            raise RuntimeError("train the model first")
+        if not temperature > 0:
+            raise ValueError("temperature must be positive")
+        x, squeeze = self._prep(data)
+        if not x.is_cuda:
+            x = x.to(self.device)
+        if ids is None:
+            ids = self.predict(data)
+        c = (self.centroids.unsqueeze(0) if squeeze else self.centroids).to(self.dtype).contiguous()
+        bias = c.float().square().sum(-1) * (-1.0 / temperature)
+        r = token_log_probs(x, c, (ids.unsqueeze(0) if squeeze else ids).to(x.device), scale=2.0 / temperature,
+                            bias=bias, top=top)
+        return type(r)(*(t[0] if squeeze and t is not None else t for t in r))
 
     def fit_predict(self, data: torch.Tensor) -> torch.Tensor:
         self.train(data)
