@@ -10,8 +10,8 @@
 // (3 F d values each) once from HBM; every expert is read for all its tokens
 // together, as the sort-inverse update gathers the points of one cluster.
 //
-// k_route: one cluster of 8 CTAs per 8 tokens.  The CTAs share the experts; a
-// thread keeps its slice of the 8 tokens in registers and meets every expert's
+// k_route: one cluster of 8 CTAs per 4 tokens.  The CTAs share the experts; a
+// thread keeps its slice of the 4 tokens in registers and meets every expert's
 // row with it.  Scores are summed in fp64 (products of 16-bit values are exact,
 // so experts are ranked by their exact scores) and sent to the CTA of their
 // token, which ranks the experts by counting the better ones.
@@ -46,6 +46,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "fk_sm100.cuh"
 
@@ -57,7 +58,8 @@ namespace cg = cooperative_groups;
 constexpr int kMaxTokens = 256;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 16;
-constexpr int kRouteCtas = 8;  // CTAs of a cluster = tokens of a cluster
+constexpr int kRouteCtas = 8;  // CTAs of a cluster
+constexpr int kRouteTokens = 4;  // its tokens
 constexpr int kWarps = 8;
 constexpr float kHalfScale = 1.f / 64.f;
 
@@ -73,6 +75,8 @@ struct MoeArgs {
   float *part;       // (T * k, d)
   int *err;
   int counters;
+  int S;  // warps per unit
+  long long early;  // bytes of w_in asked for before the routing is known
 };
 
 template <typename T>
@@ -92,6 +96,7 @@ struct Two<__nv_bfloat16> {
 
 // ------------------------------------------------------------------ routing
 constexpr int kPerCta = kMaxExperts / kRouteCtas;  // experts of one CTA at most
+constexpr int kRouteBatch = 4;                     // router rows worked on together
 
 // Order of a score as an integer; NaN ranks with -inf, below everything else.
 __device__ __forceinline__ unsigned long long score_key(double v) {
@@ -103,15 +108,15 @@ __device__ __forceinline__ unsigned long long score_key(double v) {
 
 template <typename T>
 __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(32 * kWarps) k_route(const MoeArgs a) {
-  __shared__ double part[kWarps][kPerCta][kRouteCtas];
+  __shared__ double part[kWarps][kPerCta][kRouteTokens];
   __shared__ double scores[kMaxExperts];
   __shared__ unsigned long long keys[kMaxExperts];
   __shared__ int sel[kMaxTopK];
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = (int)cluster.block_rank();
-  const int t0 = (blockIdx.x / kRouteCtas) * kRouteCtas;
-  const int nt = min(kRouteCtas, a.T - t0);
+  const int t0 = (blockIdx.x / kRouteCtas) * kRouteTokens;
+  const int nt = min(kRouteTokens, a.T - t0);
   pdl_wait();
   pdl_trigger();
   for (int i = blockIdx.x * blockDim.x + tid; i < a.counters; i += gridDim.x * blockDim.x) a.tickets[i] = 0;
@@ -120,9 +125,9 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(32 * kWarps
   const int mine = a.E > cta ? (a.E - cta + kRouteCtas - 1) / kRouteCtas : 0;  // experts cta, cta + 8, ...
   for (int k0 = 0; k0 < a.d; k0 += 8 * 32 * kWarps) {
     const int k = k0 + tid * 8;
-    double x[kRouteCtas][8];
+    double x[kRouteTokens][8];
 #pragma unroll
-    for (int t = 0; t < kRouteCtas; ++t) {
+    for (int t = 0; t < kRouteTokens; ++t) {
       if (t < nt) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (k < a.d) v = __ldg(reinterpret_cast<const uint4 *>(xs + (size_t)t * a.d + k));
@@ -135,61 +140,71 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(32 * kWarps
         }
       }
     }
-    for (int e0 = 0; e0 < mine; e0 += 4) {
-      uint4 r[4];
+    uint4 r[kRouteBatch];
+    auto fetch = [&](int e0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kRouteBatch; ++i) {
         r[i] = make_uint4(0, 0, 0, 0);
         if (e0 + i < mine && k < a.d)
           r[i] = __ldg(reinterpret_cast<const uint4 *>(rs + (size_t)(cta + (e0 + i) * kRouteCtas) * a.d + k));
       }
+    };
+    fetch(0);
+    for (int e0 = 0; e0 < mine; e0 += kRouteBatch) {
+      // the experts of a batch are independent chains of fp64 additions
+      double acc[kRouteBatch][kRouteTokens] = {};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (e0 + i >= mine) break;
-        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-        double rd[8], acc[kRouteCtas];
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = Two<T>::f(w[j]);
-          rd[2 * j] = f.x;
-          rd[2 * j + 1] = f.y;
+        for (int i = 0; i < kRouteBatch; ++i) {
+          const uint32_t w = j == 0 ? r[i].x : j == 1 ? r[i].y : j == 2 ? r[i].z : r[i].w;
+          const float2 f = Two<T>::f(w);
+          const double lo = f.x, hi = f.y;
+#pragma unroll
+          for (int t = 0; t < kRouteTokens; ++t)
+            if (t < nt) acc[i][t] = fma(x[t][2 * j + 1], hi, fma(x[t][2 * j], lo, acc[i][t]));
         }
+      }
+      if (e0 + kRouteBatch < mine) fetch(e0 + kRouteBatch);
+      if (nt == 1) {
 #pragma unroll
-        for (int t = 0; t < kRouteCtas; ++t) {
-          acc[t] = 0.0;
-          if (t < nt) {
+        for (int o = 16; o; o >>= 1)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[t] = fma(x[t][j], rd[j], acc[t]);
-          }
-        }
-        double *out = part[warp][e0 + i];
-        if (nt == 1) {
+          for (int i = 0; i < kRouteBatch; ++i) acc[i][0] += __shfl_xor_sync(0xffffffffu, acc[i][0], o);
+      } else {
+        // four sums over 32 lanes: two exchanges halve the tokens a lane carries,
+        // three more add up the eight copies; lanes 0, 8, 16, 24 hold one each
 #pragma unroll
-          for (int o = 16; o; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
-          if (lane == 0) out[0] = k0 ? out[0] + acc[0] : acc[0];
-        } else {
-          // eight sums over 32 lanes: three exchanges halve the tokens a lane
-          // carries, two more add up the four copies; lanes 0, 4, ... hold one each
+        for (int o = 2; o; o >>= 1) {
+          const bool up = lane & (o * 8);
 #pragma unroll
-          for (int o = 4; o; o >>= 1) {
-            const bool up = lane & (o * 4);
+          for (int t = 0; t < o; ++t)
 #pragma unroll
-            for (int t = 0; t < o; ++t) {
-              const double keep = up ? acc[t + o] : acc[t], give = up ? acc[t] : acc[t + o];
-              acc[t] = keep + __shfl_xor_sync(0xffffffffu, give, o * 4);
+            for (int i = 0; i < kRouteBatch; ++i) {
+              const double keep = up ? acc[i][t + o] : acc[i][t], give = up ? acc[i][t] : acc[i][t + o];
+              acc[i][t] = keep + __shfl_xor_sync(0xffffffffu, give, o * 8);
             }
-          }
-          acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
-          acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 2);
-          if ((lane & 3) == 0) out[lane >> 2] = k0 ? out[lane >> 2] + acc[0] : acc[0];
         }
+#pragma unroll
+        for (int o = 4; o; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < kRouteBatch; ++i) acc[i][0] += __shfl_xor_sync(0xffffffffu, acc[i][0], o);
+      }
+      // nt == 1: lane 0 holds the sum (of token 0); else lanes 0, 8, 16, 24
+      if ((lane & 7) == 0 && (nt > 1 || lane == 0)) {
+#pragma unroll
+        for (int i = 0; i < kRouteBatch; ++i)
+          if (e0 + i < mine) {
+            double *out = &part[warp][e0 + i][lane >> 3];
+            *out = k0 ? *out + acc[i][0] : acc[i][0];
+          }
       }
     }
   }
   __syncthreads();
   cluster.sync();  // every CTA of the cluster runs before its memory is written
-  for (int i = tid; i < mine * kRouteCtas; i += blockDim.x) {
-    const int e = i / kRouteCtas, t = i % kRouteCtas;
+  for (int i = tid; i < mine * kRouteTokens; i += blockDim.x) {
+    const int e = i / kRouteTokens, t = i % kRouteTokens;
     if (t < nt) {
       double v = 0.0;
 #pragma unroll
@@ -204,7 +219,7 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(32 * kWarps
   for (int e = tid; e < a.E; e += blockDim.x) {
     const unsigned long long key = keys[e];
     int rank = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < a.E; ++i) rank += keys[i] > key || (keys[i] == key && i < e);
     if (rank < a.k) sel[rank] = e;
   }
@@ -314,9 +329,9 @@ constexpr int kMaxNT = 4;  // tokens of one pass over a unit's weights: 32
 
 struct ExpertSmem {
   float red[kWarps][kMaxNT][4][32];    // a warp's accumulators, where warps share a unit
-  int first[kMaxExperts + 1];          // an expert's entries in `slots`
   int fill[kMaxExperts];
-  int active[kMaxExperts];
+  int active[kMaxExperts];             // the experts that any token chose
+  int first[kMaxExperts + 1];          // their entries in `slots`
   unsigned short slots[kMaxTokens * kMaxTopK];  // token * k + choice, by expert
   int n_active;
   int word[kWarps];                    // a group's ticket or verdict, handed to its warps
@@ -424,14 +439,80 @@ __device__ __forceinline__ void unit_pass(const MoeArgs &a, ExpertSmem &sm, cons
 }
 
 template <typename T, bool DOWN>
-__device__ __forceinline__ void unit(const MoeArgs &a, ExpertSmem &sm, const Group &gr, int e, int row0) {
-  const int end = sm.first[e + 1];
-  for (int base = sm.first[e]; base < end; base += 8 * kMaxNT) {
+__device__ __forceinline__ void unit(const MoeArgs &a, ExpertSmem &sm, const Group &gr, int ae, int row0) {
+  const int e = sm.active[ae], end = sm.first[ae + 1];
+  for (int base = sm.first[ae]; base < end; base += 8 * kMaxNT) {
     const int count = min(end - base, 8 * kMaxNT);
     if (count <= 8) unit_pass<T, 1, DOWN>(a, sm, gr, e, base, count, row0);
     else if (count <= 16) unit_pass<T, 2, DOWN>(a, sm, gr, e, base, count, row0);
     else unit_pass<T, 4, DOWN>(a, sm, gr, e, base, count, row0);
   }
+}
+
+// The chosen experts, by index, and their (token, choice) entries.  Every CTA
+// has the same list of experts, since tickets number them.
+__device__ __forceinline__ void list_experts(const MoeArgs &a, ExpertSmem &sm, int tid, int lane, int warp) {
+  const int slots = a.T * a.k;
+  if (slots <= 32) {  // one warp, a lane per entry
+    if (warp == 0) {
+      const int e = lane < slots ? a.ids[lane] : -1;
+      const unsigned peers = __match_any_sync(0xffffffffu, e);
+      const bool lead = lane < slots && (__ffs(peers) - 1) == lane;
+      const unsigned leads = __ballot_sync(0xffffffffu, lead);
+      // the chosen experts of lower index, and their entries
+      int off = 0, ae = 0;
+      for (unsigned m = leads; m; m &= m - 1) {
+        const int l = __ffs(m) - 1, other = __shfl_sync(0xffffffffu, e, l);
+        const unsigned p = __shfl_sync(0xffffffffu, peers, l);
+        if (other < e) {
+          off += __popc(p);
+          ++ae;
+        }
+      }
+      if (lead) {
+        sm.active[ae] = e;
+        sm.first[ae] = off;
+      }
+      if (lane < slots) sm.slots[off + __popc(peers & ((1u << lane) - 1u))] = (unsigned short)lane;
+      if (lane == 0) {
+        sm.n_active = __popc(leads);
+        sm.first[__popc(leads)] = slots;
+      }
+    }
+    __syncthreads();
+    return;
+  }
+  for (int i = tid; i < slots; i += blockDim.x) atomicAdd(&sm.fill[a.ids[i]], 1);
+  __syncthreads();
+  if (warp == 0) {
+    int off = 0, act = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < a.E ? sm.fill[e] : 0;
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (e < a.E) sm.fill[e] = off + inc - n;
+      const unsigned some = __ballot_sync(0xffffffffu, n > 0);
+      if (n > 0) {
+        const int ae = act + __popc(some & ((1u << lane) - 1u));
+        sm.active[ae] = e;
+        sm.first[ae] = off + inc - n;
+      }
+      act += __popc(some);
+      off += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      sm.first[act] = off;
+      sm.n_active = act;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < slots; i += blockDim.x) sm.slots[atomicAdd(&sm.fill[a.ids[i]], 1)] = (unsigned short)i;
+  __syncthreads();
 }
 
 // Columns [blk * 16, + 16) of y: the slots of each token, in order.  A lane
@@ -461,63 +542,38 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_experts(const MoeArgs a) {
   extern __shared__ uint8_t expert_smem[];
   ExpertSmem &sm = *reinterpret_cast<ExpertSmem *>(expert_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int slots = a.T * a.k;
+  const Group gr = {a.S, warp / a.S, warp % a.S, lane};
   for (int e = tid; e < a.E; e += blockDim.x) sm.fill[e] = 0;
   __syncthreads();
+  // where most experts will be chosen, the first units' weights are known
+  // before the routing is: they travel to L2 meanwhile
+  for (long long o = ((long long)blockIdx.x * blockDim.x + tid) * 128; o < a.early; o += (long long)gridDim.x * blockDim.x * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(a.w_in) + o));
   pdl_wait();
-  for (int i = tid; i < slots; i += blockDim.x) atomicAdd(&sm.fill[a.ids[i]], 1);
-  __syncthreads();
-  if (warp == 0) {  // offsets, and the experts that any token chose
-    int off = 0, act = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int n = e < a.E ? sm.fill[e] : 0;
-      int inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (e < a.E) sm.first[e] = sm.fill[e] = off + inc - n;
-      const unsigned some = __ballot_sync(0xffffffffu, n > 0);
-      if (n > 0) sm.active[act + __popc(some & ((1u << lane) - 1u))] = e;
-      act += __popc(some);
-      off += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) {
-      sm.first[a.E] = off;
-      sm.n_active = act;
-    }
-  }
-  __syncthreads();
-  for (int i = tid; i < slots; i += blockDim.x) sm.slots[atomicAdd(&sm.fill[a.ids[i]], 1)] = (unsigned short)i;
-  __syncthreads();
+  int t = 0;
+  if (gr.leader()) t = atomicAdd(a.tickets, 1);  // in flight while the lists are made
+  list_experts(a, sm, tid, lane, warp);
 
   const int ups = a.F / 8, downs = (a.d + 15) / 16;
   const int n_up = sm.n_active * ups, n_all = n_up + sm.n_active * downs;
   int *done_up = a.tickets + 1, *done_block = a.tickets + 1 + a.E;
-  // the fewest warps per unit that give every warp of the grid one
-  const int warps = (int)gridDim.x * kWarps, units = min(n_up, n_all - n_up);
-  int S = 1;
-  while (S < kWarps && (long long)units * S < warps) S *= 2;
-  const Group gr = {S, warp / S, warp % S, lane};
-  int t = gr.share(sm, gr.leader() ? atomicAdd(a.tickets, 1) : 0);
+  t = gr.share(sm, t);
   while (t < n_all) {
     int next = 0;
     if (gr.leader()) next = atomicAdd(a.tickets, 1);  // in flight under this unit's loads
     if (t < n_up) {
-      const int ae = t / ups, e = sm.active[ae];
-      unit<T, false>(a, sm, gr, e, (t - ae * ups) * 8);
+      const int ae = t / ups;
+      unit<T, false>(a, sm, gr, ae, (t - ae * ups) * 8);
       if (gr.leader()) {
         __threadfence();
-        atomicAdd(done_up + e, 1);
+        atomicAdd(done_up + ae, 1);
       }
     } else {
-      const int ae = (t - n_up) / downs, blk = (t - n_up) - ae * downs, e = sm.active[ae];
+      const int ae = (t - n_up) / downs, blk = (t - n_up) - ae * downs;
       int ok = 1;
-      if (gr.leader() && load_acquire(done_up + e) < ups) {
+      if (gr.leader() && load_acquire(done_up + ae) < ups) {
         const unsigned long long t0 = sm100::globaltimer();
-        while (load_acquire(done_up + e) < ups) {
+        while (load_acquire(done_up + ae) < ups) {
           if (sm100::globaltimer() - t0 > kWaitLimitNs) {
             atomicCAS(a.err, DEV_OK, DEV_TIMEOUT);
             ok = 0;
@@ -526,7 +582,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_experts(const MoeArgs a) {
         }
       }
       if (!gr.share(sm, ok)) return;
-      unit<T, true>(a, sm, gr, e, blk * 16);
+      unit<T, true>(a, sm, gr, ae, blk * 16);
       int last = 0;
       if (gr.leader()) {
         __threadfence();
@@ -566,12 +622,21 @@ size_t moe_bytes(const fk_moe_shape &m) {
 
 template <typename T>
 int launch_moe(const MoeArgs &a, cudaStream_t s) {
-  FK_CUDA(launch_pdl(k_route<T>, dim3((a.T + kRouteCtas - 1) / kRouteCtas * kRouteCtas), dim3(32 * kWarps), 0, s, a));
+  FK_CUDA(launch_pdl(k_route<T>, dim3((a.T + kRouteTokens - 1) / kRouteTokens * kRouteCtas), dim3(32 * kWarps), 0, s, a));
   FK_TRY(launched());
   FK_TRY(set_smem_limit((const void *)k_experts<T>, (int)sizeof(ExpertSmem)));
+  // the fewest warps per unit that give every warp of the grid one, for as many
+  // experts as even choices would hit
+  const double hit = a.E * (1.0 - std::pow(1.0 - (double)a.k / a.E, a.T));
+  const long long fewer = (long long)(hit * std::min(a.F / 8, (a.d + 15) / 16));
   const long long units = (long long)std::min(a.E, a.T * a.k) * (a.F / 8 + (a.d + 15) / 16);
   const int grid = (int)std::min<long long>(2LL * num_sms(), units);
-  FK_CUDA(launch_pdl(k_experts<T>, dim3(grid), dim3(32 * kWarps), sizeof(ExpertSmem), s, a));
+  MoeArgs b = a;
+  b.S = 1;
+  const long long w_in = 4LL * a.E * a.F * a.d;
+  b.early = hit >= 0.85 * a.E ? std::min(w_in, 32LL << 20) : 0;
+  while (b.S < kWarps && fewer * b.S < (long long)grid * kWarps) b.S *= 2;
+  FK_CUDA(launch_pdl(k_experts<T>, dim3(grid), dim3(32 * kWarps), sizeof(ExpertSmem), s, b));
   return launched();
 }
 
