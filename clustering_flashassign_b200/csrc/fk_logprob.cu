@@ -16,6 +16,7 @@ FwdSpace fwd_space(const Dims &m, int top, void *base) {
   if (f.L) {
     f.top_v = (float *)w.take((size_t)m.B * m.N * parts * f.L * 4);
     f.top_i = (int32_t *)w.take((size_t)m.B * m.N * parts * f.L * 4);
+    if (m.B * m.N > kJoinBlockRows) f.max_norm2 = (unsigned *)w.take((size_t)m.B * 4);
   }
   if (m.planes == 3) {
     f.xs = w.take((size_t)m.B * 3 * m.N * m.dp * 2);
@@ -106,6 +107,7 @@ int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float 
   j.parts = a.parts, j.L = f.L, j.cands = top ? std::min(m.K, top + kSpare) : 0, j.top = top;
   j.logp = logp, j.lse = lse, j.entropy = entropy, j.top_logp = top_logp, j.top_ids = top_ids;
   j.err = err;
+  j.max_norm2 = f.max_norm2;
   j.vec = m.d * esize(m.dtype) % 16 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(c)) & 15) == 0;
   return launch_join(j, m.dtype, s);
 }

@@ -160,6 +160,9 @@ struct StatArgs {
 };
 
 // Joins a row's partial results (one warp per row).
+// Up to this many rows, a row whose alternatives are asked for gets a block.
+constexpr long long kJoinBlockRows = 4096;
+
 struct JoinArgs {
   const float4 *part;
   const float *top_v;
@@ -174,6 +177,7 @@ struct JoinArgs {
   float *logp, *lse, *entropy, *top_logp;
   int32_t *top_ids;
   int *err;
+  unsigned *max_norm2;  // (B): scratch of the joins without a block per row, or NULL
 };
 
 struct Dims {
@@ -342,6 +346,7 @@ struct FwdSpace {
   float4 *part;
   float *top_v;
   int32_t *top_i;
+  unsigned *max_norm2;
   size_t bytes;
 };
 

@@ -70,8 +70,9 @@ def test_rows_with_every_column_masked():
     assert torch.isfinite(dx[0]).all() and torch.isfinite(dc[0]).all()
 
 
-def test_fewer_open_columns_than_alternatives():
-    x, c, ids = make(1, 9, 40, 32)
+@pytest.mark.parametrize("N", [9, 5000])  # a block per row, a thread per row
+def test_fewer_open_columns_than_alternatives(N):
+    x, c, ids = make(1, N, 40, 32)
     bias = torch.full((1, 40), -INF, device="cuda")
     bias[0, [31, 5]] = 0.0
     r = token_log_probs(x, c, ids * 0 + 5, bias=bias, top=6)
@@ -105,14 +106,15 @@ def test_ignored_rows_and_padding_hold_anything(dtype):
     assert (gb[0][ids < 0] == 0).all()
 
 
-def test_nan_rows_stay_their_own():
-    x, c, ids = make(1, 140, 400, 64)
+@pytest.mark.parametrize("N", [140, 5000])
+def test_nan_rows_stay_their_own(N):
+    x, c, ids = make(1, N, 400, 64)
     clean = token_log_probs(x, c, ids, top=3)
     x[0, 5] = NAN
     r = token_log_probs(x, c, ids, top=3)
     assert torch.isnan(r.logp[0, 5]) and torch.isnan(r.lse[0, 5]) and torch.isnan(r.entropy[0, 5])
     assert ((r.top_ids >= 0) & (r.top_ids < 400)).all()
-    keep = torch.arange(140, device="cuda") != 5
+    keep = torch.arange(N, device="cuda") != 5
     for a, b in zip(r, clean):
         assert torch.equal(a[0, keep], b[0, keep])
 
@@ -129,8 +131,9 @@ def test_token_out_of_range_is_ignored_and_reported():
     assert fk.fk_device_error() == fk.FK_OK
 
 
-def test_ties_go_to_the_lowest_index():
-    x, c, ids = make(1, 33, 20, 32)
+@pytest.mark.parametrize("N", [33, 5000])
+def test_ties_go_to_the_lowest_index(N):
+    x, c, ids = make(1, N, 20, 32)
     table = torch.cat([c[:, torch.randperm(20)] for _ in range(60)], 1).contiguous()  # 60 copies of each row
     r = token_log_probs(x, table, ids, top=7)
     s = x.double() @ table.double().transpose(1, 2)
