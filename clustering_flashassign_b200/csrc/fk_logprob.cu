@@ -1,4 +1,7 @@
 // Forward entry points of the token log probabilities.
+#include <mutex>
+#include <set>
+
 #include "fk_logprob.cuh"
 
 namespace fk {
@@ -10,8 +13,7 @@ FwdSpace fwd_space(const Dims &m, int top, void *base) {
   f.p = plan_runs(m.B, m.N, m.K, m.d, m.pairs, m.planes, m.dp * 2 * m.planes);
   f.L = list_length(top);
   Carve w(base);
-  const bool seg = f.p.kblocks * f.p.pairs > tile::kSegBlocks;
-  const long long parts = f.parts = stat_warps(seg, f.L) / 4 * f.p.runs;
+  const long long parts = f.parts = 3 * f.p.runs;
   f.part = (float4 *)w.take((size_t)m.B * m.N * parts * sizeof(float4));
   if (f.L) {
     f.top_v = (float *)w.take((size_t)m.B * m.N * parts * f.L * 4);
@@ -27,6 +29,21 @@ FwdSpace fwd_space(const Dims &m, int top, void *base) {
 }
 
 }  // namespace
+
+int check_registers(const void *kernel, int regs) {
+  static std::mutex mu;
+  static std::set<const void *> good;
+  std::lock_guard<std::mutex> lk(mu);
+  if (good.count(kernel)) return FK_OK;
+  cudaFuncAttributes at;
+  FK_CUDA(cudaFuncGetAttributes(&at, kernel));
+  if (at.numRegs != regs)
+    return set_error(FK_ECUDA, "tile kernel built with " + std::to_string(at.numRegs) + " registers, not " +
+                                   std::to_string(regs));
+  good.insert(kernel);
+  return FK_OK;
+}
+
 }  // namespace soft
 }  // namespace fk
 

@@ -152,7 +152,7 @@ struct StatArgs {
   const float *bias;  // (B, K) or NULL
   const int32_t *ids;
   long long N, K;
-  int parts;  // partial results per row: 2 or 3 * runs
+  int parts;  // partial results per row: 3 * runs
   int L;      // columns kept per partial list, 0: none
   float4 *part;          // (B, N, parts): m, sum, sum e (t - m), target score
   float *top_v;          // (B, N, parts, L)
@@ -273,6 +273,9 @@ inline bool too_many(const Plan &p, int B) {
   return (double)B * p.row_tiles * p.runs * p.ksplits > 2e9;
 }
 
+// The register split waits for registers that the launch must have brought.
+int check_registers(const void *kernel, int regs);
+
 template <int kCG, class Epi, bool A_MN, bool B_MN>
 int launch_group(const CUtensorMap &ta, const CUtensorMap &tb, Plan p, const typename Epi::Args &ea, size_t epi_smem,
                  int ab_fmt, int *err, cudaStream_t s) {
@@ -285,10 +288,11 @@ int launch_group(const CUtensorMap &ta, const CUtensorMap &tb, Plan p, const typ
             (B_MN ? 1u << 16 : 0u);
   const int smem = (int)(1024 + p.stages * stage + tile::kCtrlBytes + epi_smem);
   FK_TRY(set_smem_limit((const void *)kern, 227 * 1024));
+  FK_TRY(check_registers((const void *)kern, tile::kLaunchRegs));
   const int workers = std::min(num_sms() / kCG, p.units);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(workers * kCG);
-  cfg.blockDim = dim3(tile::Shape<Epi>::kThreads);
+  cfg.blockDim = dim3(tile::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -333,11 +337,6 @@ struct Carve {
 // in registers (an insertion costs five instructions a place), else 32 in
 // shared memory.
 constexpr int list_length(int top) { return top == 0 ? 0 : top + kSpare <= 16 ? (top + kSpare + 3) / 4 * 4 : 32; }
-
-// Epilogue warps of the score kernels.  Where the contraction is short the
-// epilogue's latency is the limit and a third warp per quadrant hides more of it;
-// longer lists and summed segments need the registers instead.
-constexpr int stat_warps(bool seg, int L) { return !seg && L <= 8 ? 12 : 8; }
 
 struct FwdSpace {
   Plan p;

@@ -64,7 +64,6 @@ template <typename T, bool BIAS, bool SEG>
 struct GradEpi {
   using Args = GradArgs;
   static constexpr bool kSeg = SEG;
-  static constexpr int kWarps = 8;
   const Args &a;
   const int r, lane;
   BiasTile bt;
@@ -75,9 +74,9 @@ struct GradEpi {
   T *g = nullptr;
   float *cp = nullptr;
 
-  __device__ GradEpi(const Args &args, int lane_, int r_in_tile, int half, uint8_t *smem)
+  __device__ GradEpi(const Args &args, int lane_, int r_in_tile, int third, uint8_t *smem)
       : a(args), r(r_in_tile), lane(lane_) {
-    bt.sb = reinterpret_cast<float *>(smem) + (half * 4 + r_in_tile / 32) * BiasTile::kFloats;
+    bt.sb = reinterpret_cast<float *>(smem) + (third * 4 + r_in_tile / 32) * BiasTile::kFloats;
     if (args.bound) gs = grad_scale(*args.bound);
   }
   __device__ void begin(const Unit &w, long long row0) {
@@ -90,7 +89,7 @@ struct GradEpi {
     const long long blk = (row0 + (r & ~31)) >> 5;
     cp = a.colpart && blk < a.nblk ? a.colpart + (w.b * a.nblk + blk) * a.Kp : nullptr;
   }
-  static size_t smem_bytes() { return BIAS ? kWarps * BiasTile::kFloats * 4 : 0; }
+  static size_t smem_bytes() { return BIAS ? tile::kEpiWarps * BiasTile::kFloats * 4 : 0; }
   __device__ __forceinline__ void prepare(long long col0, int stride) {
     if (BIAS) bt.load(bias, col0, stride, a.K, lane);
   }
@@ -202,7 +201,6 @@ template <typename T, bool SEG>
 struct StoreEpi {
   using Args = StoreArgs;
   static constexpr bool kSeg = SEG;
-  static constexpr int kWarps = 8;
   const Args &a;
   const int r;
   float alpha;

@@ -22,8 +22,7 @@ template <bool BIAS, bool TOP, int LREG, bool SEG>
 struct StatEpi {
   using Args = StatArgs;
   static constexpr bool kSeg = SEG;
-  static constexpr int kWarps = stat_warps(SEG, TOP ? (LREG ? LREG : 32) : 0);
-  static constexpr int kSlots = 32 * kWarps;
+  static constexpr int kSlots = 32 * tile::kEpiWarps;
   static constexpr int kCap = LREG ? LREG : 1;
   const Args &a;
   const int r, half, slot, lane;
@@ -43,13 +42,13 @@ struct StatEpi {
     float *f = reinterpret_cast<float *>(smem);
     if (BIAS) {
       bt.sb = f + (slot / 32) * BiasTile::kFloats;
-      f += kWarps * BiasTile::kFloats;
+      f += tile::kEpiWarps * BiasTile::kFloats;
     }
     lv = f + slot;
     li = reinterpret_cast<int32_t *>(f) + args.L * kSlots + slot;
   }
   static size_t smem_bytes(int L) {
-    return (BIAS ? kWarps * BiasTile::kFloats * 4 : 0) + (TOP && !LREG ? (size_t)L * kSlots * 8 : 0);
+    return (BIAS ? tile::kEpiWarps * BiasTile::kFloats * 4 : 0) + (TOP && !LREG ? (size_t)L * kSlots * 8 : 0);
   }
 
   __device__ void begin(const Unit &w, long long row0) {
@@ -181,7 +180,7 @@ struct StatEpi {
 
   __device__ void end(const Unit &w) {
     if (row >= a.N) return;
-    const long long p = at * a.parts + w.run * (kWarps / 4) + half;
+    const long long p = at * a.parts + w.run * 3 + half;
     a.part[p] = make_float4(m, sum, us, tgt);
     if (TOP && LREG) {
 #pragma unroll

@@ -15,9 +15,9 @@
 //   warp 1      one thread (of the pair's first CTA) issues tcgen05.mma,
 //               M = 128 * CG, N = 256, K = 16; two 256-column accumulators in
 //               TMEM let the next tile's products overlap this tile's epilogue,
-//   warps 2..   epilogue: two warps share each 32-row quadrant and split the
-//               tile's columns in halves, or three take every third 32 columns
-//               (the start moves from tile to tile, as 8 is not a multiple of 3).
+//   warps 4-15  epilogue: three warps share each 32-row quadrant and take every
+//               third 32 columns (the start moves from tile to tile, as 8 is
+//               not a multiple of 3).
 //
 // fp32 operands come as three bf16 planes (hi, mid, lo: 8 + 8 + 8 significant
 // bits) and the contraction runs over the six plane pairs whose product is
@@ -43,13 +43,22 @@ using namespace sm100;
 constexpr int kRows = 128;   // rows of one CTA's tile
 constexpr int kCols = 256;   // columns of a tile
 constexpr int kK = 64;       // contraction elements per stage
-// Epilogue warps: 8, with 168 registers a thread, or 12 with 128.
-template <class Epi>
-struct Shape {
-  static_assert(Epi::kWarps == 8 || Epi::kWarps == 12, "two or three warps per 32-row quadrant");
-  static_assert(Epi::kWarps == 8 || !Epi::kSeg, "segments are summed in 128 registers a thread");
-  static constexpr int kThreads = 32 * (2 + Epi::kWarps);
-};
+// Four warpgroups: one for the producer and the MMA issuer (and two idle
+// warps), three of epilogue.  The registers of a block launched with 128 a
+// thread are split 56 / 152: 128 * 4 = 56 + 3 * 152.
+constexpr int kEpiWarps = 12;
+constexpr int kFirstEpi = 4;
+constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+constexpr int kLaunchRegs = 128;
+template <int R>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
 constexpr uint32_t kABytes = kRows * kK * 2;
 // A chain of tcgen05 accumulations rounds towards zero at every step, which adds
 // up to a bias of about steps / 2 half-units of the result (3e-6 of it at 2048
@@ -233,7 +242,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // What an epilogue sees.  Epi provides
 //   struct Args                    kernel argument
 //   static constexpr bool kSeg     sum segments of the contraction in registers
-//   static constexpr int kWarps    epilogue warps
 //   begin(const Unit &, row0)      before the unit's first tile
 //   skip(column)                   warp-uniform: nothing to do from this column on
 //   prepare(column, stride)        before the wait for a tile's products: the warp's
@@ -243,7 +251,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // and is constructed per thread with (args, lane, row in CTA tile, warp of the
 // quadrant, shared memory).
 template <int CG, bool A_MN, bool B_MN, class Epi>
-__global__ void __launch_bounds__(Shape<Epi>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     k_tiles(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
             const __grid_constant__ Plan p, const __grid_constant__ typename Epi::Args ea, int *err) {
   extern __shared__ uint8_t smem_raw[];
@@ -269,7 +277,7 @@ __global__ void __launch_bounds__(Shape<Epi>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull(i), 1);
-      mbar_init(tempty(i), Epi::kWarps * CG);
+      mbar_init(tempty(i), kEpiWarps * CG);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -285,6 +293,8 @@ __global__ void __launch_bounds__(Shape<Epi>::kThreads, 1)
   pdl_wait();
   pdl_trigger();
 
+  if (warp < kFirstEpi) {
+  give_registers<56>();
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
@@ -384,9 +394,11 @@ __global__ void __launch_bounds__(Shape<Epi>::kThreads, 1)
         }
       }
     }
+  }
   } else {
-    const int quad = warp & 3, half = (warp - 2) >> 2;  // of two or three
-    Epi epi(ea, lane, quad * 32 + lane, half, ctrl_gen + kCtrlBytes);
+    take_registers<152>();
+    const int quad = warp & 3, third = (warp - kFirstEpi) >> 2;
+    Epi epi(ea, lane, quad * 32 + lane, third, ctrl_gen + kCtrlBytes);
     uint32_t n = 0;
     bool ok = true;
     auto release = [&](uint32_t buf) {
@@ -401,29 +413,28 @@ __global__ void __launch_bounds__(Shape<Epi>::kThreads, 1)
       const Unit w = unit_of(p, u);
       epi.begin(w, (w.rt * CG + (int)rank) * kRows);
       for (int ct = w.ct0; ct < w.ct1 && ok; ++ct) {
-        constexpr bool kThirds = Epi::kWarps == 12;
-        const int first = kThirds ? (half + ct) % 3 * 32 : half * (kCols / 2);
+        const int first = (third + ct) % 3 * 32;
         const long long col0 = (long long)ct * kCols + first;
         const uint32_t lanes = tmem + first + ((uint32_t)(quad * 32) << 16);
-        epi.prepare(col0, kThirds ? 96 : 32);
+        epi.prepare(col0, 96);
         if constexpr (Epi::kSeg) {
-          float sum[4][32];
+          float sum[3][32];
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch)
+          for (int i = 0; i < 3; ++i)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) sum[ch][j] = 0.f;
+            for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
           for (int ks = w.k0; ks < w.k1 && ok; ks += kSegBlocks, ++n) {
             const uint32_t buf = n & 1;
             if (!warp_wait(tfull(buf), (n >> 1) & 1, abort_flag, err, lane)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
+            for (int i = 0; i < 3; ++i) {
               uint32_t acc[32];
-              if (!epi.skip(col0 + ch * 32)) {
-                tmem_ld_32x32b_x32(lanes + buf * kCols + ch * 32, acc);
+              if (first + 96 * i < kCols && !epi.skip(col0 + 96 * i)) {
+                tmem_ld_32x32b_x32(lanes + buf * kCols + 96 * i, acc);
                 wait_ld(acc);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) sum[ch][j] += __uint_as_float(acc[j]);
+                for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(acc[j]);
               }
             }
             release(buf);
@@ -431,46 +442,28 @@ __global__ void __launch_bounds__(Shape<Epi>::kThreads, 1)
           if (ok) {
             // one copy of the epilogue's code: the sums move up instead
 #pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-              if (epi.skip(col0 + ch * 32)) break;
-              epi.chunk(sum[0], col0 + ch * 32, ch);
+            for (int i = 0; first + 96 * i < kCols; ++i) {
+              if (epi.skip(col0 + 96 * i)) break;
+              epi.chunk(sum[0], col0 + 96 * i, i);
               __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 3; ++i)
+              for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int j = 0; j < 32; ++j) sum[i][j] = sum[i + 1][j];
+                for (int j = 0; j < 32; ++j) sum[q][j] = sum[q + 1][j];
             }
           }
         } else {
           const uint32_t buf = n & 1;
           if (!warp_wait(tfull(buf), (n >> 1) & 1, abort_flag, err, lane)) { ok = false; break; }
           tc_fence_after();
-          if constexpr (kThirds) {
 #pragma unroll 1
-            for (int at = 0, i = 0; first + at < kCols; at += 96, ++i) {
-              if (epi.skip(col0 + at)) break;
-              float acc[32];
-              tmem_ld_32x32b_x32(lanes + buf * kCols + at, reinterpret_cast<uint32_t(&)[32]>(acc));
-              wait_ld(reinterpret_cast<uint32_t(&)[32]>(acc));
-              epi.chunk(acc, col0 + at, i);
-              __syncwarp();  // the next load is warp-wide
-            }
-          } else {
-            // the next 32 columns travel while these are worked on
-            uint32_t next[32];
-            if (!epi.skip(col0)) tmem_ld_32x32b_x32(lanes + buf * kCols, next);
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-              if (epi.skip(col0 + ch * 32)) break;
-              float acc[32];
-              wait_ld(next);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) acc[j] = __uint_as_float(next[j]);
-              if (ch < 3 && !epi.skip(col0 + ch * 32 + 32))
-                tmem_ld_32x32b_x32(lanes + buf * kCols + ch * 32 + 32, next);
-              epi.chunk(acc, col0 + ch * 32, ch);
-              __syncwarp();
-            }
+          for (int i = 0; first + 96 * i < kCols; ++i) {
+            if (epi.skip(col0 + 96 * i)) break;
+            float acc[32];
+            tmem_ld_32x32b_x32(lanes + buf * kCols + 96 * i, reinterpret_cast<uint32_t(&)[32]>(acc));
+            wait_ld(reinterpret_cast<uint32_t(&)[32]>(acc));
+            epi.chunk(acc, col0 + 96 * i, i);
+            __syncwarp();  // the next load is warp-wide
           }
           release(buf);
           ++n;
