@@ -64,6 +64,7 @@ template <typename T, bool BIAS, bool SEG>
 struct GradEpi {
   using Args = GradArgs;
   static constexpr bool kSeg = SEG;
+  static constexpr int kRegs = 152;
   const Args &a;
   const int r, lane;
   BiasTile bt;
@@ -201,6 +202,7 @@ template <typename T, bool SEG>
 struct StoreEpi {
   using Args = StoreArgs;
   static constexpr bool kSeg = SEG;
+  static constexpr int kRegs = 152;
   const Args &a;
   const int r;
   float alpha;

@@ -22,6 +22,7 @@ template <bool BIAS, bool TOP, int LREG, bool SEG>
 struct StatEpi {
   using Args = StatArgs;
   static constexpr bool kSeg = SEG;
+  static constexpr int kRegs = SEG && TOP ? 160 : 152;
   static constexpr int kSlots = 32 * tile::kEpiWarps;
   static constexpr int kCap = LREG ? LREG : 1;
   const Args &a;

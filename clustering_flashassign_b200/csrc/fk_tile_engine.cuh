@@ -33,6 +33,8 @@
 // rows stay in L2.
 #pragma once
 
+#include <type_traits>
+
 #include "fk_sm100.cuh"
 
 namespace fk {
@@ -45,7 +47,10 @@ constexpr int kCols = 256;   // columns of a tile
 constexpr int kK = 64;       // contraction elements per stage
 // Four warpgroups: one for the producer and the MMA issuer (and two idle
 // warps), three of epilogue.  The registers of a block launched with 128 a
-// thread are split 56 / 152: 128 * 4 = 56 + 3 * 152.
+// thread are split 56 / 152, or 32 / 160 for epilogues that keep segments and
+// lists (128 * 4 = 56 + 3 * 152 = 32 + 3 * 160): those then spill little, at the
+// price of spills around the producer's loads, which cost products without such
+// an epilogue 6% (dX and dC of N 4096, K 65536, d 2048).
 constexpr int kEpiWarps = 12;
 constexpr int kFirstEpi = 4;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
@@ -242,6 +247,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // What an epilogue sees.  Epi provides
 //   struct Args                    kernel argument
 //   static constexpr bool kSeg     sum segments of the contraction in registers
+//   static constexpr int kRegs     registers of an epilogue thread, 152 or 160
 //   begin(const Unit &, row0)      before the unit's first tile
 //   skip(column)                   warp-uniform: nothing to do from this column on
 //   prepare(column, stride)        before the wait for a tile's products: the warp's
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
 
   if (warp < kFirstEpi) {
-  give_registers<56>();
+  give_registers<4 * kLaunchRegs - 3 * Epi::kRegs>();
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0;
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   } else {
-    take_registers<152>();
+    take_registers<Epi::kRegs>();
     const int quad = warp & 3, third = (warp - kFirstEpi) >> 2;
     Epi epi(ea, lane, quad * 32 + lane, third, ctrl_gen + kCtrlBytes);
     uint32_t n = 0;
@@ -419,26 +425,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         epi.prepare(col0, 96);
         if constexpr (Epi::kSeg) {
           float sum[3][32];
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) sum[i][j] = 0.f;
-          for (int ks = w.k0; ks < w.k1 && ok; ks += kSegBlocks, ++n) {
+          auto segment = [&](auto add) {
             const uint32_t buf = n & 1;
-            if (!warp_wait(tfull(buf), (n >> 1) & 1, abort_flag, err, lane)) { ok = false; break; }
+            if (!warp_wait(tfull(buf), (n >> 1) & 1, abort_flag, err, lane)) return false;
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-              uint32_t acc[32];
               if (first + 96 * i < kCols && !epi.skip(col0 + 96 * i)) {
-                tmem_ld_32x32b_x32(lanes + buf * kCols + 96 * i, acc);
-                wait_ld(acc);
+                if constexpr (decltype(add)::value) {
+                  uint32_t acc[32];
+                  tmem_ld_32x32b_x32(lanes + buf * kCols + 96 * i, acc);
+                  wait_ld(acc);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(acc[j]);
+                  for (int j = 0; j < 32; j += 2) {
+                    const float2 v = __fadd2_rn(make_float2(sum[i][j], sum[i][j + 1]),
+                                                make_float2(__uint_as_float(acc[j]), __uint_as_float(acc[j + 1])));
+                    sum[i][j] = v.x;
+                    sum[i][j + 1] = v.y;
+                  }
+                } else {
+                  tmem_ld_32x32b_x32(lanes + buf * kCols + 96 * i, reinterpret_cast<uint32_t(&)[32]>(sum[i]));
+                }
               }
             }
+            if constexpr (!decltype(add)::value) {
+#pragma unroll
+              for (int i = 0; i < 3; ++i) wait_ld(reinterpret_cast<uint32_t(&)[32]>(sum[i]));
+            }
             release(buf);
-          }
+            ++n;
+            return true;
+          };
+          ok = segment(std::false_type{});
+          for (int ks = w.k0 + kSegBlocks; ks < w.k1 && ok; ks += kSegBlocks) ok = segment(std::true_type{});
           if (ok) {
             // one copy of the epilogue's code: the sums move up instead
 #pragma unroll 1
