@@ -82,16 +82,6 @@ __global__ void __launch_bounds__(256) k_max_norm(const T *c, long long rows, lo
 constexpr int kJoinWarps = 8;
 constexpr int kNoCol = 0x7fffffff;
 
-// One warp's joined lists (and the row's candidates with their exact scores)
-// where eight warps share a row.
-struct JoinRow {
-  float m[kJoinWarps], s[kJoinWarps], u[kJoinWarps], tgt[kJoinWarps];
-  float v[kJoinWarps][32];
-  int k[kJoinWarps][32];
-  int cand[32];
-  double exact[32];
-};
-
 // The best `n` of the lanes' sorted lists of up to LL columns (k < 0: the end);
 // lane j of the group keeps the j-th.  The lists move up as their heads go.
 template <int LPR, int LL>
@@ -166,28 +156,9 @@ __device__ __forceinline__ float rank_error(const JoinArgs &a, long long b, floa
   return 2.f * ((steps + 4.f) * 1.2e-7f * size + 1e-6f * fabsf(v)) + 1e-37f;
 }
 
-// LPR lanes of WPR warps per row.  (8, 1): many rows of few parts, four rows a
-// warp; (32, 1); (32, 8): few rows, whose exact scores would otherwise be one
-// warp's long chain of loads.
-template <typename T, int LPR, int WPR, int LL>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
-  __shared__ JoinRow sh;
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & (LPR - 1);
-  const int sub = WPR > 1 ? warp : 0;  // this warp among the row's warps
-  const long long per_block = WPR > 1 ? 1 : kJoinWarps * (32 / LPR);
-  const long long r0 = (long long)blockIdx.x * per_block + (WPR > 1 ? 0 : threadIdx.x / LPR);
-  // lanes of a row beyond the last one follow along on the last row
-  const bool live = r0 < a.rows;
-  const long long r = live ? r0 : a.rows - 1;
-  const long long b = r / a.N;
-  const int first = sub * LPR + lane, step = LPR * WPR;
-  float m = kNegInf, s = 0.f, u = 0.f, tgt = kNegInf;
-  for (int p = first; p < a.parts; p += step) {
-    const float4 q = a.part[r * a.parts + p];
-    join_stats(m, s, u, q.x, q.y, q.z);
-    tgt = fmaxf(tgt, q.w);
-  }
+// Joins the statistics of LPR lanes; all of them hold the result.
+template <int LPR>
+__device__ __forceinline__ void reduce_stats(float &m, float &s, float &u, float &tgt, int lane) {
 #pragma unroll
   for (int o = LPR / 2; o; o >>= 1) {
     const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
@@ -202,23 +173,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
     }
     tgt = fmaxf(tgt, __shfl_xor_sync(0xffffffffu, tgt, o));
   }
-  if (WPR > 1) {
-    if (lane == 0) {
-      sh.m[warp] = m, sh.s[warp] = s, sh.u[warp] = u, sh.tgt[warp] = tgt;
-    }
-    __syncthreads();
-    m = sh.m[0], s = sh.s[0], u = sh.u[0], tgt = sh.tgt[0];
-    for (int w = 1; w < WPR; ++w) {
-      join_stats(m, s, u, sh.m[w], sh.s[w], sh.u[w]);
-      tgt = fmaxf(tgt, sh.tgt[w]);
-    }
+}
+
+// LPR lanes per row.
+template <typename T, int LPR, int LL>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
+  pdl_wait();
+  const int lane = threadIdx.x & (LPR - 1);
+  const long long r0 = (long long)blockIdx.x * (kJoinWarps * (32 / LPR)) + threadIdx.x / LPR;
+  // lanes of a row beyond the last one follow along on the last row
+  const bool live = r0 < a.rows;
+  const long long r = live ? r0 : a.rows - 1;
+  const long long b = r / a.N;
+  float m = kNegInf, s = 0.f, u = 0.f, tgt = kNegInf;
+  for (int p = lane; p < a.parts; p += LPR) {
+    const float4 q = a.part[r * a.parts + p];
+    join_stats(m, s, u, q.x, q.y, q.z);
+    tgt = fmaxf(tgt, q.w);
   }
+  reduce_stats<LPR>(m, s, u, tgt, lane);
   // a row whose columns are all masked has lse = -inf and an entropy of zero
   const bool none = m == kNegInf && s == 0.f;
   const float ls = log2f(s);
-  if (live && lane == 0 && sub == 0) {
-    write_stats(a, r, m, s, u, tgt, none, ls);
-  }
+  if (live && lane == 0) write_stats(a, r, m, s, u, tgt, none, ls);
   if (a.top == 0) return;
 
   // the lane's own list: its parts' lists, joined (LL columns at most)
@@ -229,48 +206,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
     hv[i] = kNegInf;
     hk[i] = -1;
   }
-  for (int p = first; p < a.parts; p += step) {
-    const float4 *pv = reinterpret_cast<const float4 *>(a.top_v + (r * a.parts + p) * a.L);
-    const int4 *pk = reinterpret_cast<const int4 *>(a.top_i + (r * a.parts + p) * a.L);
-    float nv[LL];
-    int nk[LL];
-#pragma unroll
-    for (int i = 0; i < LL / 4; ++i) {
-      const float4 v = __ldg(pv + i);
-      const int4 k = __ldg(pk + i);
-      nv[4 * i] = v.x, nv[4 * i + 1] = v.y, nv[4 * i + 2] = v.z, nv[4 * i + 3] = v.w;
-      nk[4 * i] = k.x, nk[4 * i + 1] = k.y, nk[4 * i + 2] = k.z, nk[4 * i + 3] = k.w;
-    }
-    if (p == first) {
-#pragma unroll
-      for (int i = 0; i < LL; ++i) {
-        hv[i] = nv[i];
-        hk[i] = nk[i];
-      }
-    } else {
-#pragma unroll(LL <= 16 ? LL : 1)
-      for (int j = 0; j < LL; ++j) {
-        insert_ordered<LL>(hv, hk, nv[j], nk[j]);
-      }
+  for (int p = lane; p < a.parts; p += LPR) {
+    const float *pv = a.top_v + (r * a.parts + p) * a.L;
+    const int32_t *pk = a.top_i + (r * a.parts + p) * a.L;
+#pragma unroll 1
+    for (int j = 0; j < LL; ++j) {
+      const int k = __ldg(pk + j);
+      if (k < 0) break;
+      insert_ordered<LL>(hv, hk, __ldg(pv + j), k);
     }
   }
+  __syncwarp();
   draw<LPR, LL>(a.cands, lane, hv, hk, mv, mine);
-  if (WPR > 1) {
-    sh.v[warp][lane] = mv;
-    sh.k[warp][lane] = mine;
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int i = 0; i < LL; ++i) {
-        hv[i] = lane < WPR ? sh.v[lane < WPR ? lane : 0][i] : kNegInf;
-        hk[i] = lane < WPR ? sh.k[lane < WPR ? lane : 0][i] : -1;
-      }
-      draw<LPR, LL>(a.cands, lane, hv, hk, mv, mine);
-    }
-  }
   const unsigned group = LPR == 32 ? 0u : (threadIdx.x & 31) & ~(LPR - 1u);  // first lane of the row's group
   const unsigned mask = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << group;
-  if (sub == 0) {
+  {
     // masked (or NaN) columns are in no list: they follow, lowest index first
     const int found = __popc(__ballot_sync(0xffffffffu, mine >= 0) & mask);
     if (__any_sync(0xffffffffu, found < a.cands)) {
@@ -287,14 +237,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
       }
     }
   }
-  if (WPR > 1) {
-    if (warp == 0) sh.cand[lane] = mine;
-    __syncthreads();
-  }
   const T *x = static_cast<const T *>(a.x) + (size_t)r * a.d;
   const T *c = static_cast<const T *>(a.c) + (size_t)b * a.K * a.d;
   const float *bias = a.bias ? a.bias + b * a.K : nullptr;
-  if (WPR == 1 && a.max_norm2) {
+  if (a.max_norm2) {
     // many rows: see rank_error
     float n2 = 0.f;
     if (a.vec) {
@@ -322,26 +268,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
     }
   }
   double v = (double)kNegInf;
-  if (WPR > 1) {  // candidates warp, warp + 8, ...
-    if (warp < a.cands) {
-      int k[4];
-      double e[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) k[i] = sh.cand[warp + 8 * i < a.cands ? warp + 8 * i : warp];
-      if (a.cands <= 8) {
-        const int k1[1] = {k[0]};
-        double e1[1];
-        exact_scores<T, LPR, 1>(x, c, bias, a.scale, k1, a.d, a.vec, lane, e1);
-        e[0] = e1[0];
-      } else {
-        exact_scores<T, LPR, 4>(x, c, bias, a.scale, k, a.d, a.vec, lane, e);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane == 0 && warp + 8 * i < a.cands) sh.exact[warp + 8 * i] = e[i];
-    }
-  } else {
-    for (int j = 0; j < a.cands; j += 4) {
+  for (int j = 0; j < a.cands; j += 4) {
       int k[4];
       double e[4];
 #pragma unroll
@@ -350,12 +277,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (lane == j + i) v = e[i];
-    }
-  }
-  if (WPR > 1) {
-    __syncthreads();
-    if (warp != 0) return;
-    if (lane < a.cands) v = sh.exact[lane];
   }
   const double rank_v = v == v ? v : (double)kNegInf;
   int rank = 0;
@@ -366,6 +287,141 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
   }
   if (live && lane < a.cands && rank < a.top) {
     write_top(a, r, rank, mine, v, m, s, none, ls);
+  }
+}
+
+
+// A block per row, for few rows: their lists are too many for a warp, and their
+// exact scores would be one warp's long chain of loads.  The code is kept small
+// rather than unrolled: one row runs it once, out of a cold instruction cache.
+//
+// Columns are ordered by a 64-bit key (score, then lowest index).  Every thread
+// has the best of its lists; the cands-th best of these is a bound, and only
+// columns at or above it are gathered (cands threads' lists at most) and ranked.
+constexpr int kMaxParts = 3 * 2 * 160;  // of one row: three per run
+constexpr int kGather = 32 * 32 * ((kMaxParts + 255) / 256);
+
+__device__ __forceinline__ unsigned long long column_key(float v, int k) {
+  if (k < 0) return 0ull;
+  const unsigned b = __float_as_uint(v == 0.f ? 0.f : v);
+  const unsigned o = b & 0x80000000u ? ~b : b | 0x80000000u;
+  return ((unsigned long long)o << 32) | (0xffffffffu - (unsigned)k);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a) {
+  __shared__ float st[4][kJoinWarps];
+  __shared__ unsigned long long heads[kJoinWarps * 32], bound, found[kGather];
+  __shared__ int n_found, cand[32];
+  __shared__ double exact[32];
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long r = blockIdx.x, b = r / a.N;
+  if (tid == 0) {
+    n_found = 0;
+    bound = 0ull;
+  }
+  float m = kNegInf, s = 0.f, u = 0.f, tgt = kNegInf;
+  unsigned long long head = 0ull;
+  for (int p = tid; p < a.parts; p += 32 * kJoinWarps) {
+    const float4 q = __ldg(a.part + r * a.parts + p);
+    const long long o = (r * a.parts + p) * a.L;
+    head = max(head, column_key(__ldg(a.top_v + o), __ldg(a.top_i + o)));
+    join_stats(m, s, u, q.x, q.y, q.z);
+    tgt = fmaxf(tgt, q.w);
+  }
+  reduce_stats<32>(m, s, u, tgt, lane);
+  if (lane == 0) st[0][warp] = m, st[1][warp] = s, st[2][warp] = u, st[3][warp] = tgt;
+  // the warp's best heads, in order
+  unsigned long long left = head;
+#pragma unroll 1
+  for (int j = 0; j < a.cands; ++j) {
+    const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(left >> 32));
+    const unsigned lo = __reduce_max_sync(0xffffffffu, (unsigned)(left >> 32) == hi ? (unsigned)left : 0u);
+    const unsigned long long best = ((unsigned long long)hi << 32) | lo;
+    if (lane == 0) heads[warp * a.cands + j] = best;
+    if (left == best) left = 0ull;
+  }
+  __syncthreads();
+  m = st[0][0], s = st[1][0], u = st[2][0], tgt = st[3][0];
+#pragma unroll 1
+  for (int w = 1; w < kJoinWarps; ++w) {
+    join_stats(m, s, u, st[0][w], st[1][w], st[2][w]);
+    tgt = fmaxf(tgt, st[3][w]);
+  }
+  const bool none = m == kNegInf && s == 0.f;
+  const float ls = log2f(s);
+  if (tid == 0) write_stats(a, r, m, s, u, tgt, none, ls);
+  if (tid < kJoinWarps * a.cands) {
+    const unsigned long long mine = heads[tid];
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < kJoinWarps * a.cands; ++i) rank += heads[i] > mine;
+    if (rank == a.cands - 1 && mine) bound = mine;  // keys differ: one thread at most
+  }
+  __syncthreads();
+  const unsigned long long least = bound;
+  if (head && head >= least) {
+#pragma unroll 1
+    for (int p = tid; p < a.parts; p += 32 * kJoinWarps) {
+      const long long o = (r * a.parts + p) * a.L;
+#pragma unroll 1
+      for (int j = 0; j < a.L; ++j) {  // sorted: the rest is lower
+        const unsigned long long key = column_key(__ldg(a.top_v + o + j), __ldg(a.top_i + o + j));
+        if (!key || key < least) break;
+        found[atomicAdd(&n_found, 1)] = key;
+      }
+    }
+  }
+  __syncthreads();
+  const int n = n_found;
+#pragma unroll 1
+  for (int i = tid; i < n; i += 32 * kJoinWarps) {
+    const unsigned long long mine = found[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += found[j] > mine;
+    if (rank < a.cands) cand[rank] = (int)(0xffffffffu - (unsigned)mine);
+  }
+  __syncthreads();
+  if (n < a.cands) {  // masked (or NaN) columns are in no list: they follow, lowest index first
+    if (tid == 0) {
+      int next = 0;
+      for (int i = n; i < a.cands; ++i, ++next) {
+        for (int j = 0; j < n; ++j)
+          if (cand[j] == next) {
+            ++next;
+            j = -1;
+          }
+        cand[i] = next;
+      }
+    }
+    __syncthreads();
+  }
+  const T *x = static_cast<const T *>(a.x) + (size_t)r * a.d;
+  const T *c = static_cast<const T *>(a.c) + (size_t)b * a.K * a.d;
+  const float *bias = a.bias ? a.bias + b * a.K : nullptr;
+#pragma unroll 1
+  for (int j = warp; j < a.cands; j += 2 * kJoinWarps) {  // candidates j and j + 8
+    const int other = j + kJoinWarps < a.cands ? j + kJoinWarps : j;
+    const int k[2] = {cand[j], cand[other]};
+    double e[2];
+    exact_scores<T, 32, 2>(x, c, bias, a.scale, k, a.d, a.vec, lane, e);
+    if (lane == 0) {
+      exact[j] = e[0];
+      if (other != j) exact[other] = e[1];
+    }
+  }
+  __syncthreads();
+  if (tid < a.cands) {
+    const double v = exact[tid], rank_v = v == v ? v : (double)kNegInf;
+    int rank = 0;
+#pragma unroll 1
+    for (int j = 0; j < a.cands; ++j) {
+      const double w = exact[j], wv = w == w ? w : (double)kNegInf;
+      rank += wv > rank_v || (wv == rank_v && cand[j] < cand[tid]);
+    }
+    if (rank < a.top) write_top(a, r, rank, cand[tid], v, m, s, none, ls);
   }
 }
 
@@ -494,18 +550,18 @@ __global__ void __launch_bounds__(256) k_join_rows(const JoinArgs a) {
   }
 }
 
-template <typename T, int LPR, int WPR, int LL>
+template <typename T, int LPR, int LL>
 int launch_join_as(const JoinArgs &j, cudaStream_t s) {
-  const int per_block = WPR > 1 ? 1 : kJoinWarps * (32 / LPR);
-  FK_CUDA(launch_pdl(k_join<T, LPR, WPR, LL>, dim3((unsigned)cdiv(j.rows, per_block)), dim3(32 * kJoinWarps), 0, s, j));
+  FK_CUDA(launch_pdl(k_join<T, LPR, LL>, dim3((unsigned)cdiv(j.rows, kJoinWarps * (32 / LPR))), dim3(32 * kJoinWarps), 0,
+                     s, j));
   return launched();
 }
 
-// A block per row while the rows alone do not fill the SMs; a thread per row
-// where there are many, of few parts (604800 rows of 3 parts, top 4: 185 us against 246
-// by 8 lanes a row); else as many lanes as there are candidates, at least 8.
+// Many rows: a thread per row where its parts are few (604800 rows of 3 parts,
+// top 4: 185 us against 246 by 8 lanes a row); else as many lanes as there are
+// candidates, at least 8.
 template <typename T, int LL>
-int launch_join_list(const JoinArgs &j, cudaStream_t s) {
+int launch_join_many(const JoinArgs &j, cudaStream_t s) {
   if (j.max_norm2) {
     FK_CUDA(cudaMemsetAsync(j.max_norm2, 0, (size_t)(j.rows / j.N) * sizeof(unsigned), s));
     const long long rows = j.rows / j.N * j.K;
@@ -513,24 +569,32 @@ int launch_join_list(const JoinArgs &j, cudaStream_t s) {
                        j.K, j.d, j.max_norm2));
     FK_TRY(launched());
   }
-  if (j.rows > kJoinBlockRows && j.parts <= 8 && LL <= 16) {
-    const dim3 grid((unsigned)cdiv(j.rows, 256));
-    if (j.L) FK_CUDA(launch_pdl(k_join_rows<T, LL <= 16 ? LL : 16>, grid, dim3(256), 0, s, j));
-    else FK_CUDA(launch_pdl(k_join_rows<T, 0>, grid, dim3(256), 0, s, j));
-    return launched();
+  if constexpr (LL <= 16) {
+    if (j.rows > kJoinBlockRows && j.parts <= 8) {
+      const dim3 grid((unsigned)cdiv(j.rows, 256));
+      if (j.L) FK_CUDA(launch_pdl(k_join_rows<T, LL>, grid, dim3(256), 0, s, j));
+      else FK_CUDA(launch_pdl(k_join_rows<T, 0>, grid, dim3(256), 0, s, j));
+      return launched();
+    }
   }
-  if (j.L && j.rows <= kJoinBlockRows) return launch_join_as<T, 32, 8, LL>(j, s);
-  if (j.cands <= 8 && j.parts <= 64) return launch_join_as<T, 8, 1, LL>(j, s);
-  if (j.cands <= 16) return launch_join_as<T, 16, 1, LL>(j, s);
-  return launch_join_as<T, 32, 1, LL>(j, s);
+  if (j.cands <= 8 && j.parts <= 64) return launch_join_as<T, 8, LL>(j, s);
+  if (j.cands <= 16 && j.parts <= 64) return launch_join_as<T, 16, LL>(j, s);
+  return launch_join_as<T, 32, LL>(j, s);
 }
 
+// A block per row while the rows alone do not fill the SMs.
 template <typename T>
 int launch_join_typed(const JoinArgs &j, cudaStream_t s) {
-  if (j.L <= 4) return launch_join_list<T, 4>(j, s);
-  if (j.L == 8) return launch_join_list<T, 8>(j, s);
-  if (j.L <= 16) return j.L == 12 ? launch_join_list<T, 12>(j, s) : launch_join_list<T, 16>(j, s);
-  return launch_join_list<T, 32>(j, s);
+  if (j.L && j.rows <= kJoinBlockRows) {
+    if (j.parts > kMaxParts) return set_error(FK_EUNSUPPORTED, "too many partial results per row");
+    FK_CUDA(launch_pdl(k_join_block<T>, dim3((unsigned)j.rows), dim3(32 * kJoinWarps), 0, s, j));
+    return launched();
+  }
+  if (j.L <= 4) return launch_join_many<T, 4>(j, s);
+  if (j.L == 8) return launch_join_many<T, 8>(j, s);
+  if (j.L == 12) return launch_join_many<T, 12>(j, s);
+  if (j.L == 16) return launch_join_many<T, 16>(j, s);
+  return launch_join_many<T, 32>(j, s);
 }
 
 }  // namespace
