@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -328,7 +329,7 @@ def _soft_shape(where, x, c):
     if x.dim() != 3 or c.dim() != 3:
         raise ValueError(f"{where}: x must be (B, N, d) and c (B, K, d)")
     (B, N, d), K = x.shape, c.shape[1]
-    return FkShape(B, N, K, d, _dtype_code(x)), B, N, K, d
+    return (B, N, K, d, _dtype_code(x)), B, N, K, d
 
 
 def fk_logprob(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, logp: torch.Tensor, lse: torch.Tensor,
@@ -355,16 +356,21 @@ def fk_logprob(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, logp: torch.
     return logp
 
 
+@functools.lru_cache(maxsize=1024)
+def _logprob_bytes(device_index, B, N, K, d, dtype, top) -> int:
+    """fk_logprob_workspace: a function of the sizes and the device."""
+    need = ctypes.c_longlong(0)
+    _check(lib.fk_logprob_workspace(ctypes.byref(FkShape(B, N, K, d, dtype)), top, ctypes.byref(need)), "fk_logprob")
+    return need.value
+
+
 def _call_logprob(shape, dev, args, workspace=None, stream=None) -> None:
-    """lib.fk_logprob on checked arguments."""
-    w = "fk_logprob"
+    """lib.fk_logprob on checked arguments; shape = (B, N, K, d, dtype)."""
     with _at(dev):
-        need = ctypes.c_longlong(0)
-        if st := lib.fk_logprob_workspace(ctypes.byref(shape), args[8], ctypes.byref(need)):
-            _check(st, w)
-        workspace, pw, n = _scratch(w, workspace, need.value, dev, stream)
-        if st := lib.fk_logprob(ctypes.byref(shape), *args, pw, n, _handle(stream, dev)):
-            _check(st, w)
+        need = _logprob_bytes(dev.index, *shape, args[8])
+        workspace, pw, n = _scratch("fk_logprob", workspace, need, dev, stream)
+        if st := lib.fk_logprob(FkShape(*shape), *args, pw, n, _handle(stream, dev)):
+            _check(st, "fk_logprob")
 
 
 def fk_logprob_backward(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, lse: torch.Tensor, entropy=None,
@@ -383,14 +389,20 @@ def fk_logprob_backward(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, lse
     pdx, pdc = _need(w, "dx", dx, dt, (B, N, d), dev), _need(w, "dc", dc, dt, (B, K, d), dev)
     pdb = _need(w, "dbias", dbias, f32, (B, K), dev)
     with _at(dev):
-        need = ctypes.c_longlong(0)
-        if st := lib.fk_logprob_backward_workspace(ctypes.byref(shape), bias is not None, dbias is not None,
-                                                   ctypes.byref(need)):
+        need = _grad_bytes(dev.index, *shape, bias is not None, dbias is not None)
+        workspace, pw, n = _scratch(w, workspace, need, dev, stream)
+        if st := lib.fk_logprob_backward(FkShape(*shape), px, pc, pb, scale, pi, ps, pe, ga, gl, ge, pdx, pdc, pdb, pw, n,
+                                         _handle(stream, dev)):
             _check(st, w)
-        workspace, pw, n = _scratch(w, workspace, need.value, dev, stream)
-        if st := lib.fk_logprob_backward(ctypes.byref(shape), px, pc, pb, scale, pi, ps, pe, ga, gl, ge, pdx, pdc, pdb,
-                                         pw, n, _handle(stream, dev)):
-            _check(st, w)
+
+
+@functools.lru_cache(maxsize=1024)
+def _grad_bytes(device_index, B, N, K, d, dtype, bias, dbias) -> int:
+    """fk_logprob_backward_workspace: a function of the sizes and the device."""
+    need = ctypes.c_longlong(0)
+    _check(lib.fk_logprob_backward_workspace(ctypes.byref(FkShape(B, N, K, d, dtype)), bias, dbias, ctypes.byref(need)),
+           "fk_logprob_backward")
+    return need.value
 
 
 def fk_moe(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, y: torch.Tensor,
@@ -412,21 +424,25 @@ def fk_moe(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_out: tor
     pin, pout = _need(w, "w_in", w_in, dt, (E, 2 * F, d), dev), _need(w, "w_out", w_out, dt, (E, d, F), dev)
     py, pi = _need(w, "y", y, dt, (T, d), dev), _need(w, "expert_ids", expert_ids, torch.int32, (T, k), dev)
     pg = _need(w, "expert_weights", expert_weights, torch.float32, (T, k), dev)
-    shape = FkMoeShape(T, E, d, F, k, _dtype_code(x), act, bool(renormalize))
+    shape = (T, E, d, F, k, _dtype_code(x), act, int(bool(renormalize)))
     _call_moe(shape, dev, (px, pr, pin, pout, py, pi, pg), workspace, stream)
     return y
 
 
+@functools.lru_cache(maxsize=1024)
+def _moe_bytes(*shape) -> int:
+    """fk_moe_workspace: a function of the sizes."""
+    need = ctypes.c_longlong(0)
+    _check(lib.fk_moe_workspace(ctypes.byref(FkMoeShape(*shape)), ctypes.byref(need)), "fk_moe")
+    return need.value
+
+
 def _call_moe(shape, dev, args, workspace=None, stream=None) -> None:
-    """lib.fk_moe on checked arguments."""
-    w = "fk_moe"
+    """lib.fk_moe on checked arguments; shape = (T, E, d, F, top_k, dtype, act, renormalize)."""
     with _at(dev):
-        need = ctypes.c_longlong(0)
-        if st := lib.fk_moe_workspace(ctypes.byref(shape), ctypes.byref(need)):
-            _check(st, w)
-        workspace, pw, n = _scratch(w, workspace, need.value, dev, stream)
-        if st := lib.fk_moe(ctypes.byref(shape), *args, pw, n, _handle(stream, dev)):
-            _check(st, w)
+        workspace, pw, n = _scratch("fk_moe", workspace, _moe_bytes(*shape), dev, stream)
+        if st := lib.fk_moe(FkMoeShape(*shape), *args, pw, n, _handle(stream, dev)):
+            _check(st, "fk_moe")
 
 
 def fk_device_error(stream=None) -> int:

@@ -22,7 +22,7 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (DTYPES, FK_ACT_GELU, FK_ACT_SILU, FkMoeShape, FkShape, _call_logprob, _call_moe,
+from . import (DTYPES, FK_ACT_GELU, FK_ACT_SILU, _call_logprob, _call_moe,
                fk_logprob_backward)
 
 
@@ -50,7 +50,7 @@ def _forward(x, c, bias, ids, scale, top):
         top_ids = x.new_empty((B, N, top), dtype=torch.int32)
         top_logp = x.new_empty((B, N, top), dtype=torch.float32)
         pi, pl = top_ids.data_ptr(), top_logp.data_ptr()
-    _call_logprob(FkShape(B, N, K, d, DTYPES[x.dtype]), dev,
+    _call_logprob((B, N, K, d, DTYPES[x.dtype]), dev,
                   (x.data_ptr(), c.data_ptr(), None if bias is None else bias.data_ptr(), scale, ids.data_ptr(),
                    logp.data_ptr(), lse.data_ptr(), entropy.data_ptr(), top, pi, pl))
     return logp, lse, entropy, top_ids, top_logp
@@ -155,10 +155,12 @@ def expert_mixture(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_
     k, d, (E, _, F), dt, dev = int(top_k), x.shape[-1], w_out.shape, x.dtype, x.device
     if not x.is_cuda or dt not in DTYPES:
         raise ValueError(f"x must be an fp16 or bf16 CUDA tensor, got {dt} on {dev}")
-    for name, t, shape in (("router", router, (E, d)), ("w_in", w_in, (E, 2 * F, d)), ("w_out", w_out, (E, d, F))):
-        if t.dtype != dt or t.shape != shape or t.device != dev:
-            raise ValueError(f"{name} must be {dt} of shape {shape} on {dev}, got {t.dtype} of shape "
-                             f"{tuple(t.shape)} on {t.device}")
+    if (router.dtype != dt or w_in.dtype != dt or w_out.dtype != dt or router.shape != (E, d)
+            or w_in.shape != (E, 2 * F, d) or w_out.shape != (E, d, F)):
+        raise ValueError(f"router, w_in and w_out must be {dt} of shapes {(E, d)}, {(E, 2 * F, d)}, {(E, d, F)}: got "
+                         + ", ".join(f"{t.dtype} {tuple(t.shape)}" for t in (router, w_in, w_out)))
+    if router.device != dev or w_in.device != dev or w_out.device != dev:
+        raise ValueError(f"x is on {dev}, the weights on {router.device}, {w_in.device}, {w_out.device}")
     flat = x.dim() == 2
     xs = (x if flat else x.reshape(-1, d)).contiguous()
     router, w_in, w_out = router.contiguous(), w_in.contiguous(), w_out.contiguous()
@@ -166,7 +168,7 @@ def expert_mixture(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_
     y = torch.empty_like(xs)
     ids = xs.new_empty((T, k), dtype=torch.int32)
     weights = xs.new_empty((T, k), dtype=torch.float32)
-    _call_moe(FkMoeShape(T, E, d, F, k, DTYPES[dt], _ACTIVATIONS[activation], bool(renormalize)), dev,
+    _call_moe((T, E, d, F, k, DTYPES[dt], _ACTIVATIONS[activation], int(bool(renormalize))), dev,
               (xs.data_ptr(), router.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), y.data_ptr(), ids.data_ptr(),
                weights.data_ptr()))
     if flat:
