@@ -110,9 +110,9 @@ def _load():
                                       ctypes.POINTER(FkOptions)]),
         "fk_update_finalize": (I, [P, P, I, I, I, I, P, P, P, P]),
         "fk_inject_fault": (I, [I, LL]),
-        "fk_logprob": (I, [ctypes.POINTER(FkShape), P, P, P, F, P, P, P, P, I, P, P, P, LL, P]),
+        "fk_logprob": (I, [ctypes.POINTER(FkShape), P, P, P, F, P, P, P, P, P, I, P, P, P, LL, P]),
         "fk_logprob_workspace": (I, [ctypes.POINTER(FkShape), I, ctypes.POINTER(LL)]),
-        "fk_logprob_backward": (I, [ctypes.POINTER(FkShape), P, P, P, F, P, P, P, P, P, P, P, P, P, P, LL, P]),
+        "fk_logprob_backward": (I, [ctypes.POINTER(FkShape), P, P, P, F, P, P, P, P, P, P, P, P, P, P, P, LL, P]),
         "fk_moe": (I, [ctypes.POINTER(FkMoeShape), P, P, P, P, P, P, P, P, LL, P]),
         "fk_moe_workspace": (I, [ctypes.POINTER(FkMoeShape), ctypes.POINTER(LL)]),
         "fk_logprob_backward_workspace": (I, [ctypes.POINTER(FkShape), I, I, ctypes.POINTER(LL)]),
@@ -334,10 +334,10 @@ def _soft_shape(where, x, c):
 
 def fk_logprob(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, logp: torch.Tensor, lse: torch.Tensor,
                entropy=None, top_ids=None, top_logp=None, bias=None, scale: float = 1.0, workspace=None,
-               stream=None) -> torch.Tensor:
+               stream=None, lse_rest=None) -> torch.Tensor:
     """logp[b,n] = s[ids[b,n]] - logsumexp(s), s = scale x.c^T + bias; lse, entropy and the best columns with it.
 
-    x (B,N,d), c (B,K,d), ids (B,N) int32, bias (B,K) fp32; logp / lse / entropy (B,N) fp32,
+    x (B,N,d), c (B,K,d), ids (B,N) int32, bias (B,K) fp32; logp / lse / lse_rest / entropy (B,N) fp32,
     top_ids / top_logp (B,N,top) int32 / fp32.  workspace: a uint8 tensor of at least
     fk_logprob_workspace bytes (None: allocated here)."""
     w = "fk_logprob"
@@ -349,10 +349,10 @@ def fk_logprob(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, logp: torch.
     px, pc = _need(w, "x", x, x.dtype, (B, N, d), dev), _need(w, "c", c, x.dtype, (B, K, d), dev)
     pb, pi = _need(w, "bias", bias, f32, (B, K), dev), _need(w, "ids", ids, i32, row, dev)
     pl, ps = _need(w, "logp", logp, f32, row, dev), _need(w, "lse", lse, f32, row, dev)
-    pe = _need(w, "entropy", entropy, f32, row, dev)
+    pr, pe = _need(w, "lse_rest", lse_rest, f32, row, dev), _need(w, "entropy", entropy, f32, row, dev)
     pti = _need(w, "top_ids", top_ids, i32, (B, N, top), dev)
     ptl = _need(w, "top_logp", top_logp, f32, (B, N, top), dev)
-    _call_logprob(shape, dev, (px, pc, pb, scale, pi, pl, ps, pe, top, pti, ptl), workspace, stream)
+    _call_logprob(shape, dev, (px, pc, pb, scale, pi, pl, ps, pr, pe, top, pti, ptl), workspace, stream)
     return logp
 
 
@@ -367,7 +367,7 @@ def _logprob_bytes(device_index, B, N, K, d, dtype, top) -> int:
 def _call_logprob(shape, dev, args, workspace=None, stream=None) -> None:
     """lib.fk_logprob on checked arguments; shape = (B, N, K, d, dtype)."""
     with _at(dev):
-        need = _logprob_bytes(dev.index, *shape, args[8])
+        need = _logprob_bytes(dev.index, *shape, args[9])
         workspace, pw, n = _scratch("fk_logprob", workspace, need, dev, stream)
         if st := lib.fk_logprob(FkShape(*shape), *args, pw, n, _handle(stream, dev)):
             _check(st, "fk_logprob")
@@ -375,7 +375,7 @@ def _call_logprob(shape, dev, args, workspace=None, stream=None) -> None:
 
 def fk_logprob_backward(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, lse: torch.Tensor, entropy=None,
                         dlogp=None, dlse=None, dentropy=None, dx=None, dc=None, dbias=None, bias=None,
-                        scale: float = 1.0, workspace=None, stream=None) -> None:
+                        scale: float = 1.0, workspace=None, stream=None, lse_rest=None) -> None:
     """Gradients of fk_logprob into dx (B,N,d), dc (B,K,d) (x's dtype) and dbias (B,K) fp32, each optional,
     from upstream gradients dlogp, dlse, dentropy (B,N) fp32, each optional."""
     w = "fk_logprob_backward"
@@ -385,13 +385,14 @@ def fk_logprob_backward(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, lse
     pb, pi = _need(w, "bias", bias, f32, (B, K), dev), _need(w, "ids", ids, torch.int32, row, dev)
     ps, pe = _need(w, "lse", lse, f32, row, dev), _need(w, "entropy", entropy, f32, row, dev)
     ga, gl = _need(w, "dlogp", dlogp, f32, row, dev), _need(w, "dlse", dlse, f32, row, dev)
-    ge = _need(w, "dentropy", dentropy, f32, row, dev)
+    ge, pr = _need(w, "dentropy", dentropy, f32, row, dev), _need(w, "lse_rest", lse_rest, f32, row, dev)
     pdx, pdc = _need(w, "dx", dx, dt, (B, N, d), dev), _need(w, "dc", dc, dt, (B, K, d), dev)
     pdb = _need(w, "dbias", dbias, f32, (B, K), dev)
     with _at(dev):
         need = _grad_bytes(dev.index, *shape, bias is not None, dbias is not None)
         workspace, pw, n = _scratch(w, workspace, need, dev, stream)
-        if st := lib.fk_logprob_backward(FkShape(*shape), px, pc, pb, scale, pi, ps, pe, ga, gl, ge, pdx, pdc, pdb, pw, n,
+        if st := lib.fk_logprob_backward(FkShape(*shape), px, pc, pb, scale, pi, ps, pr, pe, ga, gl, ge, pdx, pdc, pdb, pw,
+                                         n,
                                          _handle(stream, dev)):
             _check(st, w)
 

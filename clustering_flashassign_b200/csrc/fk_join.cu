@@ -11,7 +11,7 @@ __device__ __forceinline__ void join_stats(float &m, float &s, float &u, float m
   // an empty side has s = u = 0 and its (clamped) distance contributes nothing;
   // a NaN sum stays NaN
   const float d1 = fmaxf(m - ms, kLowest), d2 = fmaxf(m2 - ms, kLowest);
-  const float f1 = ex2(m - ms), f2 = ex2(m2 - ms);
+  const float f1 = pow2(m - ms), f2 = pow2(m2 - ms);  // the m are whole numbers
   u = f1 * fmaf(d1, s, u) + f2 * fmaf(d2, s2, u2);
   s = f1 * s + f2 * s2;
   m = mm;
@@ -127,21 +127,56 @@ __device__ __forceinline__ void insert_ordered(float (&hv)[LL], int (&hk)[LL], f
   }
 }
 
-__device__ __forceinline__ void write_stats(const JoinArgs &a, long long r, float m, float s, float u, float tgt,
-                                            bool none, float ls) {
+// A row's joined statistics: lse = m + ls in base 2 with m whole and ls in [0, 1)
+// (ls = log2 of the sum's significand), so that a confident row's log
+// probability is a small difference of small numbers.
+struct RowStat {
+  float m, ls, hs;  // hs = (sum e (t - m)) / sum
+  bool none;        // every column is masked: lse = -inf, entropy 0
+  bool nan;
+};
+
+__device__ __forceinline__ RowStat row_stat(float m, float s, float u) {
+  RowStat r;
+  r.none = m == kNegInf && s == 0.f;
+  r.nan = !(s == s);
+  r.hs = u / s;
+  if (s > 0.f && s < INFINITY) {
+    const int e = ilogbf(s);
+    r.m = m + (float)e;
+    r.ls = log2f(scalbnf(s, -e));
+    r.hs -= (float)e;
+  } else {
+    r.m = m;
+    r.ls = log2f(s);
+  }
+  return r;
+}
+
+// Log probability of a stored score (a product, or in base 2 with a bias).
+__device__ __forceinline__ float stored_logp(const JoinArgs &a, const RowStat &q, float v) {
+  if (q.none || (v == kNegInf && !q.nan)) return kNegInf;
+  const float rel = a.bias ? v - q.m : fmaf(v, a.scale * kLog2e, -q.m);
+  return -at_least_0((q.ls - rel) * kLn2);
+}
+
+__device__ __forceinline__ void write_stats(const JoinArgs &a, long long r, const RowStat &q, float tgt) {
   const int id = a.ids[r];
   const bool valid = id >= 0 && id < a.K;
   if (id >= a.K) atomicCAS(a.err, DEV_OK, DEV_BAD_ID);
-  a.lse[r] = none ? kNegInf : (m + ls) * kLn2;
-  if (a.entropy) a.entropy[r] = none ? 0.f : at_least_0((ls - u / s) * kLn2);
-  a.logp[r] = !valid ? 0.f : (none || (tgt == kNegInf && s == s)) ? kNegInf : -at_least_0((ls - (tgt - m)) * kLn2);
+  const double lse = q.none ? (double)kNegInf : ((double)q.m + (double)q.ls) * M_LN2;
+  a.lse[r] = (float)lse;
+  if (a.lse_rest) {
+    const float rest = (float)(lse - (double)(float)lse);
+    a.lse_rest[r] = rest == rest ? rest : 0.f;
+  }
+  if (a.entropy) a.entropy[r] = q.none ? 0.f : at_least_0((q.ls - q.hs) * kLn2);
+  a.logp[r] = valid ? stored_logp(a, q, tgt) : 0.f;
 }
 
-__device__ __forceinline__ void write_top(const JoinArgs &a, long long r, int rank, int k, double v, float m, float s,
-                                          bool none, float ls) {
-  const float lp = (float)(v - (double)(none ? kNegInf : m) * M_LN2) - ls * kLn2;
+__device__ __forceinline__ void write_top(const JoinArgs &a, long long r, int rank, int k, float v, const RowStat &q) {
   a.top_ids[r * a.top + rank] = k;
-  a.top_logp[r * a.top + rank] = v == (double)kNegInf && s == s ? kNegInf : -at_least_0(-lp);
+  a.top_logp[r * a.top + rank] = stored_logp(a, q, v);
 }
 
 // Twice what a stored score v of a row of squared norm n2 can be off: the
@@ -192,10 +227,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
     tgt = fmaxf(tgt, q.w);
   }
   reduce_stats<LPR>(m, s, u, tgt, lane);
-  // a row whose columns are all masked has lse = -inf and an entropy of zero
-  const bool none = m == kNegInf && s == 0.f;
-  const float ls = log2f(s);
-  if (live && lane == 0) write_stats(a, r, m, s, u, tgt, none, ls);
+  const RowStat st = row_stat(m, s, u);
+  if (live && lane == 0) write_stats(a, r, st, tgt);
   if (a.top == 0) return;
 
   // the lane's own list: its parts' lists, joined (LL columns at most)
@@ -261,8 +294,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
     const bool close = lane < a.cands && (mv == kNegInf || (lane < a.top && lane + 1 < a.cands && !(mv - next > off)));
     if (!__any_sync(0xffffffffu, close)) {
       if (live && lane < a.top) {
-        a.top_ids[r * a.top + lane] = mine;
-        a.top_logp[r * a.top + lane] = -at_least_0((ls - (mv * (bias ? 1.f : a.scale * kLog2e) - m)) * kLn2);
+        write_top(a, r, lane, mine, mv, st);
       }
       return;
     }
@@ -286,7 +318,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
     rank += v2 > rank_v || (v2 == rank_v && k2 < mine);
   }
   if (live && lane < a.cands && rank < a.top) {
-    write_top(a, r, rank, mine, v, m, s, none, ls);
+    write_top(a, r, rank, mine, mv, st);
   }
 }
 
@@ -308,9 +340,14 @@ __device__ __forceinline__ unsigned long long column_key(float v, int k) {
   return ((unsigned long long)o << 32) | (0xffffffffu - (unsigned)k);
 }
 
+__device__ __forceinline__ float key_score(unsigned long long key) {
+  const unsigned o = (unsigned)(key >> 32);
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a) {
-  __shared__ float st[4][kJoinWarps];
+  __shared__ float parts[4][kJoinWarps], stored[32];
   __shared__ unsigned long long heads[kJoinWarps * 32], bound, found[kGather];
   __shared__ int n_found, cand[32];
   __shared__ double exact[32];
@@ -331,7 +368,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a
     tgt = fmaxf(tgt, q.w);
   }
   reduce_stats<32>(m, s, u, tgt, lane);
-  if (lane == 0) st[0][warp] = m, st[1][warp] = s, st[2][warp] = u, st[3][warp] = tgt;
+  if (lane == 0) parts[0][warp] = m, parts[1][warp] = s, parts[2][warp] = u, parts[3][warp] = tgt;
   // the warp's best heads, in order
   unsigned long long left = head;
 #pragma unroll 1
@@ -343,15 +380,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a
     if (left == best) left = 0ull;
   }
   __syncthreads();
-  m = st[0][0], s = st[1][0], u = st[2][0], tgt = st[3][0];
+  m = parts[0][0], s = parts[1][0], u = parts[2][0], tgt = parts[3][0];
 #pragma unroll 1
   for (int w = 1; w < kJoinWarps; ++w) {
-    join_stats(m, s, u, st[0][w], st[1][w], st[2][w]);
-    tgt = fmaxf(tgt, st[3][w]);
+    join_stats(m, s, u, parts[0][w], parts[1][w], parts[2][w]);
+    tgt = fmaxf(tgt, parts[3][w]);
   }
-  const bool none = m == kNegInf && s == 0.f;
-  const float ls = log2f(s);
-  if (tid == 0) write_stats(a, r, m, s, u, tgt, none, ls);
+  const RowStat st = row_stat(m, s, u);
+  if (tid == 0) write_stats(a, r, st, tgt);
   if (tid < kJoinWarps * a.cands) {
     const unsigned long long mine = heads[tid];
     int rank = 0;
@@ -381,7 +417,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a
     int rank = 0;
 #pragma unroll 4
     for (int j = 0; j < n; ++j) rank += found[j] > mine;
-    if (rank < a.cands) cand[rank] = (int)(0xffffffffu - (unsigned)mine);
+    if (rank < a.cands) {
+      cand[rank] = (int)(0xffffffffu - (unsigned)mine);
+      stored[rank] = key_score(mine);
+    }
   }
   __syncthreads();
   if (n < a.cands) {  // masked (or NaN) columns are in no list: they follow, lowest index first
@@ -394,6 +433,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a
             j = -1;
           }
         cand[i] = next;
+        stored[i] = kNegInf;
       }
     }
     __syncthreads();
@@ -421,7 +461,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a
       const double w = exact[j], wv = w == w ? w : (double)kNegInf;
       rank += wv > rank_v || (wv == rank_v && cand[j] < cand[tid]);
     }
-    if (rank < a.top) write_top(a, r, rank, cand[tid], v, m, s, none, ls);
+    if (rank < a.top) write_top(a, r, rank, cand[tid], stored[tid], st);
   }
 }
 
@@ -440,9 +480,8 @@ __global__ void __launch_bounds__(256) k_join_rows(const JoinArgs a) {
     join_stats(m, s, u, q.x, q.y, q.z);
     tgt = fmaxf(tgt, q.w);
   }
-  const bool none = m == kNegInf && s == 0.f;
-  const float ls = log2f(s);
-  if (live) write_stats(a, r, m, s, u, tgt, none, ls);
+  const RowStat st = row_stat(m, s, u);
+  if (live) write_stats(a, r, st, tgt);
   if (LL == 0) return;
 
   float hv[C];
@@ -492,13 +531,9 @@ __global__ void __launch_bounds__(256) k_join_rows(const JoinArgs a) {
       close |= !(hv[i] - hv[i + 1 < C ? i + 1 : i] > rank_error<T>(a, b, n2, bias != nullptr, hv[i]));
   }
   if (live && !close) {
-    const float unit = bias ? 1.f : a.scale * kLog2e;
 #pragma unroll
     for (int i = 0; i < C; ++i)
-      if (i < a.top) {
-        a.top_ids[r * a.top + i] = hk[i];
-        a.top_logp[r * a.top + i] = -at_least_0((ls - (hv[i] * unit - m)) * kLn2);
-      }
+      if (i < a.top) write_top(a, r, i, hk[i], hv[i], st);
   }
   // rows whose order is open, one after another by the whole warp
   for (unsigned open = __ballot_sync(0xffffffffu, live && close); open; open &= open - 1) {
@@ -544,7 +579,7 @@ __global__ void __launch_bounds__(256) k_join_rows(const JoinArgs a) {
           const double vj = ev[j] == ev[j] ? ev[j] : (double)kNegInf;
           rank += j < a.cands && (vj > vi || (vj == vi && hk[j] < hk[i]));
         }
-        if (i < a.cands && rank < a.top) write_top(a, r, rank, hk[i], ev[i], m, s, none, ls);
+        if (i < a.cands && rank < a.top) write_top(a, r, rank, hk[i], hv[i], st);
       }
     }
   }

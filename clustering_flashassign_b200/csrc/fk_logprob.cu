@@ -63,7 +63,7 @@ int fk_logprob_workspace(const fk_shape *shape, int top, long long *bytes) {
 }
 
 int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float *bias, float scale, const int32_t *ids,
-               float *logp, float *lse, float *entropy, int top, int32_t *top_ids, float *top_logp, void *workspace,
+               float *logp, float *lse, float *lse_rest, float *entropy, int top, int32_t *top_ids, float *top_logp, void *workspace,
                long long workspace_bytes, fk_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   FK_TRY(check_soft(shape, scale));
@@ -88,6 +88,7 @@ int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float 
   FK_TRY(check_dev(ids, "ids"));
   FK_TRY(check_dev(logp, "logp"));
   FK_TRY(check_dev(lse, "lse"));
+  FK_TRY(check_dev_opt(lse_rest, "lse_rest"));
   FK_TRY(check_dev_opt(entropy, "entropy"));
   if (top) {
     FK_TRY(check_dev(top_ids, "top_ids"));
@@ -122,7 +123,7 @@ int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float 
   j.ids = ids, j.x = x, j.c = c, j.bias = bias, j.scale = scale;
   j.rows = m.B * m.N, j.N = m.N, j.K = m.K, j.d = m.d;
   j.parts = a.parts, j.L = f.L, j.cands = top ? std::min(m.K, top + kSpare) : 0, j.top = top;
-  j.logp = logp, j.lse = lse, j.entropy = entropy, j.top_logp = top_logp, j.top_ids = top_ids;
+  j.logp = logp, j.lse = lse, j.lse_rest = lse_rest, j.entropy = entropy, j.top_logp = top_logp, j.top_ids = top_ids;
   j.err = err;
   j.max_norm2 = f.max_norm2;
   j.vec = m.d * esize(m.dtype) % 16 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(c)) & 15) == 0;

@@ -64,6 +64,10 @@ __device__ __forceinline__ float ex2(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// 2^n of a whole n <= 0 (0 below the normal range), exactly.
+__device__ __forceinline__ float pow2(float n) {
+  return n >= -126.f ? __int_as_float(((int)n + 127) << 23) : 0.f;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -141,10 +145,12 @@ __device__ __forceinline__ bool scores32(const float (&r)[32], float scale2, con
   }
 }
 
-struct RowGrad {  // one row's coefficients
-  float a, l, e, lse2, h;
-  int id;
-  int pad0, pad1;
+// One row's coefficients: G_k = p (c1 + c2 log2 p) + a 1[k = id], p = 2^(t_k - lse2).
+// lse in base 2 is lse2 and a remainder below its rounding; c1 and c2 carry it.
+struct RowGrad {
+  float a, c1, c2, lse2;
+  int id;  // -1: no target, -2: G is zero whatever the scores hold
+  int pad0, pad1, pad2;
 };
 
 struct StatArgs {
@@ -154,7 +160,7 @@ struct StatArgs {
   long long N, K;
   int parts;  // partial results per row: 3 * runs
   int L;      // columns kept per partial list, 0: none
-  float4 *part;          // (B, N, parts): m, sum, sum e (t - m), target score
+  float4 *part;          // (B, N, parts): m, sum, sum e (t - m), target score (as scores32 gives it)
   float *top_v;          // (B, N, parts, L)
   int32_t *top_i;
 };
@@ -174,7 +180,7 @@ struct JoinArgs {
   long long rows, N, K;
   int d, parts, L, cands, top;  // L: length of a partial list; cands = min(K, top + kSpare)
   bool vec;  // rows of x and c can be read 16 bytes at a time
-  float *logp, *lse, *entropy, *top_logp;
+  float *logp, *lse, *lse_rest, *entropy, *top_logp;
   int32_t *top_ids;
   int *err;
   unsigned *max_norm2;  // (B): scratch of the joins without a block per row, or NULL

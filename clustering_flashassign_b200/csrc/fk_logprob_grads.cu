@@ -11,7 +11,7 @@ namespace {
 // bound of |G| over the rows (float bits; positive floats order as integers).
 template <typename T>
 __global__ void __launch_bounds__(256)
-    k_rows(const int32_t *ids, const float *lse, const float *entropy, const float *dlogp, const float *dlse,
+    k_rows(const int32_t *ids, const float *lse, const float *lse_rest, const float *entropy, const float *dlogp, const float *dlse,
            const float *dent, long long rows, long long rows_per_b, int K, RowGrad *out, unsigned *bound, const T *x,
            int d, int dp, void *xs, int *err) {
   pdl_wait();
@@ -23,17 +23,19 @@ __global__ void __launch_bounds__(256)
   if (g.id >= K && lane == 0) atomicCAS(err, DEV_OK, DEV_BAD_ID);
   if (g.id < 0 || g.id >= K) g.id = -1;
   g.a = dlogp && g.id >= 0 ? dlogp[r] : 0.f;
-  g.l = dlse ? dlse[r] : 0.f;
-  g.e = dent ? dent[r] : 0.f;
-  g.h = dent ? entropy[r] : 0.f;
+  float l = dlse ? dlse[r] : 0.f, e = dent ? dent[r] : 0.f;
   const float v = lse[r];
-  g.lse2 = v * kLog2e;
-  if (v == kNegInf) g.a = g.l = g.e = 0.f;  // every column is masked
-  if (g.a == 0.f && g.l == 0.f && g.e == 0.f) g.id = -2;  // G is zero whatever the scores hold
+  if (v == kNegInf) g.a = l = e = 0.f;  // every column is masked
+  if (g.a == 0.f && l == 0.f && e == 0.f) g.id = -2;
+  const double lse2 = ((double)v + (lse_rest ? (double)lse_rest[r] : 0.0)) * 1.4426950408889634;
+  g.lse2 = (float)lse2;
+  const float lo = v == kNegInf ? 0.f : (float)(lse2 - (double)g.lse2), f = exp2f(-lo);
+  g.c1 = f * (l - g.a - e * (dent ? entropy[r] : 0.f) + e * kLn2 * lo);
+  g.c2 = -f * e * kLn2;
   if (lane == 0) {
     out[r] = g;
     // |p (log p + H)| <= max(1 / e, log K) <= log K + 1
-    const float big = fabsf(g.a) + fabsf(g.l) + fabsf(g.e) * (logf((float)K) + 1.f);
+    const float big = fabsf(g.a) + fabsf(l) + fabsf(e) * (logf((float)K) + 1.f);
     if (bound && big > 0.f) atomicMax(bound, __float_as_uint(big));
   }
   copy_row<T>(x, r, rows_per_b, d, dp, g.id == -2, xs, lane);
@@ -99,10 +101,8 @@ struct GradEpi {
     {
       float v[32];
       const bool some_masked = scores32<BIAS>(acc, a.scale2, bt, i, col, a.K, v);
-      // y = p (l - a - e (log p + H)) = p (c1 + c2 log2 p)
       const float2 nl = make_float2(-q.lse2, -q.lse2), sc = make_float2(a.scale2, a.scale2);
-      const float2 c1 = make_float2(q.l - q.a - q.e * q.h, q.l - q.a - q.e * q.h);
-      const float2 c2 = make_float2(-q.e * kLn2, -q.e * kLn2);
+      const float2 c1 = make_float2(q.c1, q.c1), c2 = make_float2(q.c2, q.c2);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float2 w = make_float2(v[2 * j], v[2 * j + 1]);
@@ -468,8 +468,8 @@ int fk_logprob_backward_workspace(const fk_shape *shape, int with_bias, int with
 }
 
 int fk_logprob_backward(const fk_shape *shape, const void *x, const void *c, const float *bias, float scale,
-                        const int32_t *ids, const float *lse, const float *entropy, const float *dlogp,
-                        const float *dlse, const float *dentropy, void *dx, void *dc, float *dbias, void *workspace,
+                        const int32_t *ids, const float *lse, const float *lse_rest, const float *entropy,
+                        const float *dlogp, const float *dlse, const float *dentropy, void *dx, void *dc, float *dbias, void *workspace,
                         long long workspace_bytes, fk_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   FK_TRY(check_soft(shape, scale));
@@ -503,6 +503,7 @@ int fk_logprob_backward(const fk_shape *shape, const void *x, const void *c, con
   FK_TRY(check_dev_opt(bias, "bias"));
   FK_TRY(check_dev(ids, "ids"));
   FK_TRY(check_dev(lse, "lse"));
+  FK_TRY(check_dev_opt(lse_rest, "lse_rest"));
   FK_TRY(check_dev_opt(entropy, "entropy"));
   FK_TRY(check_dev_opt(dlogp, "dlogp"));
   FK_TRY(check_dev_opt(dlse, "dlse"));
@@ -517,8 +518,8 @@ int fk_logprob_backward(const fk_shape *shape, const void *x, const void *c, con
   if (bound) FK_CUDA(cudaMemsetAsync(bound, 0, 16, s));
   auto prepare = [&](auto tag) -> int {
     using T = decltype(tag);
-    FK_CUDA(launch_pdl(k_rows<T>, dim3((unsigned)cdiv(rows, 8)), dim3(256), 0, s, ids, lse, entropy, dlogp, dlse,
-                       dentropy, rows, m.N, m.K, f.rows, bound, static_cast<const T *>(x), m.d, m.dp, f.xs, err));
+    FK_CUDA(launch_pdl(k_rows<T>, dim3((unsigned)cdiv(rows, 8)), dim3(256), 0, s, ids, lse, lse_rest, entropy, dlogp,
+                       dlse, dentropy, rows, m.N, m.K, f.rows, bound, static_cast<const T *>(x), m.d, m.dp, f.xs, err));
     return launched();
   };
   if (m.dtype == FK_F32) FK_TRY(prepare(float{}));

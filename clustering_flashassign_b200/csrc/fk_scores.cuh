@@ -9,8 +9,9 @@ namespace soft {
 
 // Running statistics of one row per thread.
 //
-// The sums refer to a maximum that follows the row's with a slack of 2^8: a
-// chunk's exponentials then rarely wait for its maximum.
+// The sums refer to a whole number m that follows the row's maximum with a slack
+// of 2: a chunk's exponentials then rarely wait for its maximum, and moving m
+// multiplies the sums by a power of two, without a rounding.
 //
 // The best columns.  Eight columns of which no row of the warp wants anything
 // (their maximum beats none of the lists) cost a comparison.  Otherwise they
@@ -135,13 +136,14 @@ struct StatEpi {
     }
     const float cm = max3(fmaxf(g[0], g[1]), g[2], g[3]);
     const float c2 = BIAS ? cm : cm * a.scale2;
-    if (c2 > m + 8.f) {  // always the case for the first finite chunk
+    if (c2 > m + 2.f) {  // always the case for the first finite chunk
+      const float up = ceilf(c2);
       if (m != kNegInf) {
-        const float f = ex2(m - c2);
-        us = f * fmaf(m - c2, sum, us);
+        const float f = pow2(m - up);
+        us = f * fmaf(m - up, sum, us);
         sum *= f;
       }
-      m = c2;
+      m = up;
     }
     const float ms = m == kNegInf ? 0.f : m;
     const float2 ref = make_float2(-ms, -ms), sc = make_float2(a.scale2, a.scale2);
@@ -171,7 +173,7 @@ struct StatEpi {
     if (__any_sync(0xffffffffu, rel < 32u)) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
-        if (rel == (unsigned)j) tgt = BIAS ? t[j] : t[j] * a.scale2;
+        if (rel == (unsigned)j) tgt = t[j];
     }
     if (TOP && __any_sync(0xffffffffu, cm > thr)) {
 #pragma unroll

@@ -34,7 +34,7 @@ class TokenLogProbs(NamedTuple):
     top_logp: Optional[torch.Tensor]
 
 
-def _forward(x, c, bias, ids, scale, top):
+def _forward(x, c, bias, ids, scale, top, rest=None):
     (B, N, d), K, dev = x.shape, c.shape[1], x.device
     if not x.is_cuda or x.dtype not in DTYPES:
         raise ValueError(f"x must be an fp16, bf16 or fp32 CUDA tensor, got {x.dtype} on {dev}")
@@ -52,12 +52,13 @@ def _forward(x, c, bias, ids, scale, top):
         pi, pl = top_ids.data_ptr(), top_logp.data_ptr()
     _call_logprob((B, N, K, d, DTYPES[x.dtype]), dev,
                   (x.data_ptr(), c.data_ptr(), None if bias is None else bias.data_ptr(), scale, ids.data_ptr(),
-                   logp.data_ptr(), lse.data_ptr(), entropy.data_ptr(), top, pi, pl))
+                   logp.data_ptr(), lse.data_ptr(), None if rest is None else rest.data_ptr(), entropy.data_ptr(),
+                   top, pi, pl))
     return logp, lse, entropy, top_ids, top_logp
 
 
 def _backward(ctx, dlogp, dlse, dentropy, *_):
-    x, c, bias, ids, lse, entropy = ctx.saved_tensors
+    x, c, bias, ids, lse, rest, entropy = ctx.saved_tensors
     if dlogp is None and dlse is None and dentropy is None:
         return (None,) * 6
     up = [None if g is None else g.contiguous() for g in (dlogp, dlse, dentropy)]
@@ -65,7 +66,7 @@ def _backward(ctx, dlogp, dlse, dentropy, *_):
     dx = torch.empty_like(x) if want[0] else None
     dc = torch.empty_like(c) if want[1] else None
     dbias = torch.empty_like(bias) if want[2] else None
-    fk_logprob_backward(x, c, ids, lse, entropy, *up, dx, dc, dbias, bias, ctx.scale)
+    fk_logprob_backward(x, c, ids, lse, entropy, *up, dx, dc, dbias, bias, ctx.scale, lse_rest=rest)
     return dx, dc, dbias, None, None, None
 
 
@@ -75,8 +76,9 @@ _backward_once = once_differentiable(_backward)
 class _LogProbs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, c, bias, ids, scale, top):
-        out = _forward(x, c, bias, ids, scale, top)
-        ctx.save_for_backward(x, c, bias, ids, out[1], out[2])
+        rest = x.new_empty(ids.shape, dtype=torch.float32)
+        out = _forward(x, c, bias, ids, scale, top, rest)
+        ctx.save_for_backward(x, c, bias, ids, out[1], rest, out[2])
         ctx.scale = scale
         ctx.set_materialize_grads(False)
         if top:

@@ -314,6 +314,8 @@ int fk_noalloc_device_error(fk_stream_t stream);
  * (B, N, d) meet a table c (B, K, d) (a vocabulary, a codebook, centroids):
  *     s[b,n,k] = scale * x[b,n] . c[b,k] + bias[b,k]
  *     lse      = log sum_k exp(s)                     (B, N) fp32
+ *     lse_rest = what fp32 leaves of it (lse + lse_rest is the logarithm to about
+ *                1e-7), for the gradients; nullable
  *     logp     = s[b,n,ids[b,n]] - lse                (B, N) fp32
  *     entropy  = -sum_k p log p, p = exp(s - lse)     (B, N) fp32, nullable
  *     top_ids, top_logp  the `top` largest s, lowest index on ties (ordered by
@@ -336,8 +338,8 @@ int fk_noalloc_device_error(fk_stream_t stream);
  * their own.  Nothing is allocated.
  */
 int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float *bias, float scale,
-               const int32_t *ids, float *logp, float *lse, float *entropy, int top, int32_t *top_ids,
-               float *top_logp, void *workspace, long long workspace_bytes, fk_stream_t stream);
+               const int32_t *ids, float *logp, float *lse, float *lse_rest, float *entropy, int top,
+               int32_t *top_ids, float *top_logp, void *workspace, long long workspace_bytes, fk_stream_t stream);
 int fk_logprob_workspace(const fk_shape *shape, int top, long long *bytes);
 
 /*
@@ -348,15 +350,16 @@ int fk_logprob_workspace(const fk_shape *shape, int top, long long *bytes);
  *     dc   = scale G^T x      (B, K, d) in the inputs' type
  *     dbias = sum_n G         (B, K) fp32
  * Each result is nullable (not computed).  lse and entropy are the forward
- * call's (entropy only with dentropy).  Ignored rows get nothing from dlogp; a
+ * call's (entropy only with dentropy; lse_rest nullable: p is then off by lse's
+ * rounding).  Ignored rows get nothing from dlogp; a
  * row without any upstream gradient gets zeros and contributes nothing, whatever
  * it holds; masked columns get zeros and contribute nothing.  Results are
  * bit-reproducible: no atomics touch them.  Workspace as in fk_logprob; it holds
  * G in the inputs' type for a block of rows, 4 GiB at most (256 rows at least).
  */
 int fk_logprob_backward(const fk_shape *shape, const void *x, const void *c, const float *bias, float scale,
-                        const int32_t *ids, const float *lse, const float *entropy, const float *dlogp,
-                        const float *dlse, const float *dentropy, void *dx, void *dc, float *dbias,
+                        const int32_t *ids, const float *lse, const float *lse_rest, const float *entropy,
+                        const float *dlogp, const float *dlse, const float *dentropy, void *dx, void *dc, float *dbias,
                         void *workspace, long long workspace_bytes, fk_stream_t stream);
 int fk_logprob_backward_workspace(const fk_shape *shape, int with_bias, int with_dbias, long long *bytes);
 

@@ -20,13 +20,14 @@ def need(shape, top=0):
 
 def forward(shape, x=P, c=P, bias=None, scale=1.0, ids=P, logp=P, lse=P, ent=P, top=0, ti=None, tl=None, ws=P,
             n=1 << 40):
-    return fk.lib.fk_logprob(ctypes.byref(shape), x, c, bias, scale, ids, logp, lse, ent, top, ti, tl, ws, n, None)
+    return fk.lib.fk_logprob(ctypes.byref(shape), x, c, bias, scale, ids, logp, lse, None, ent, top, ti, tl, ws, n,
+                             None)
 
 
 def backward(shape, x=P, c=P, bias=None, scale=1.0, ids=P, lse=P, ent=P, a=P, el=None, e=None, dx=P, dc=P, db=None,
              ws=P, n=1 << 40):
-    return fk.lib.fk_logprob_backward(ctypes.byref(shape), x, c, bias, scale, ids, lse, ent, a, el, e, dx, dc, db, ws,
-                                      n, None)
+    return fk.lib.fk_logprob_backward(ctypes.byref(shape), x, c, bias, scale, ids, lse, None, ent, a, el, e, dx, dc, db,
+                                      ws, n, None)
 
 
 @pytest.mark.parametrize("B,N,K,d,dtype,status", [
