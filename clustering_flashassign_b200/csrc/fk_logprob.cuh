@@ -17,7 +17,7 @@
 // All row statistics are fp32, in base 2 (scale and bias carry log2 e).
 //
 // The backward pass recomputes each tile of scores, turns it into G rounded
-// once to the operands' type (bf16: relative 2^-9 of each value; fp16: 2^-11
+// once to the operands' type (in two parts in small calls; bf16: relative 2^-9 of each value; fp16: 2^-11
 // after a power-of-two scale that brings the largest possible |G| of the call
 // to 2^14; fp32: three bf16 planes, 2^-25), and multiplies G with C and X.
 // G is held for a block of rows at a time, sized by a fixed budget.
@@ -191,6 +191,7 @@ struct Dims {
   long long N;
   int K, d, dtype;
   int planes, pairs, dp;
+  int g_planes, g_pairs;  // of G, and of its products
   long long Kp;
 };
 
@@ -199,6 +200,14 @@ inline Dims dims_of(const fk_shape &sh) {
   m.B = sh.B, m.N = sh.N, m.K = sh.K, m.d = sh.d, m.dtype = sh.dtype;
   m.planes = sh.dtype == FK_F32 ? 3 : 1;
   m.pairs = sh.dtype == FK_F32 ? 6 : 1;
+  // G is rounded once, which for a row or two can show (their gradients may be
+  // differences of a few large terms): where it costs nothing to speak of, G is
+  // kept in two parts, and the rounding of the result is the only one.  The
+  // products of one such call take 10 us at most, or read the table for 64 rows
+  // at most.
+  const double work = (double)sh.B * sh.N * sh.K * sh.d;
+  m.g_planes = m.planes == 3 ? 3 : work <= 2147483648.0 || sh.N <= 64 ? 2 : 1;
+  m.g_pairs = m.planes == 3 ? 6 : m.g_planes;
   m.dp = (sh.d + 7) / 8 * 8;
   m.Kp = ((long long)sh.K + 63) / 64 * 64;
   return m;
@@ -228,7 +237,7 @@ inline Plan plan_runs(int B, long long rows, long long cols, int kdim, int pairs
   p.col_tiles = (int)cdiv(cols, tile::kCols);
   p.kblocks = (int)cdiv(kdim, tile::kK);
   p.pairs = pairs;
-  p.planes = planes;
+  p.planes_a = p.planes_b = planes;
   p.ksplits = 1;
   double best = 1e30;
   p.runs = 1;
@@ -248,7 +257,7 @@ inline Plan plan_runs(int B, long long rows, long long cols, int kdim, int pairs
 
 // One tile per unit, the contraction split so that the last round is not
 // mostly idle; a split costs about eight K-blocks (its partial sums).
-inline Plan plan_splits(int B, long long rows, long long cols, long long kdim, int pairs, int planes) {
+inline Plan plan_splits(int B, long long rows, long long cols, long long kdim, int pairs, int planes_a, int planes_b) {
   Plan p = {};
   const double depth = std::max(1.0, pairs * cdiv(kdim, tile::kK) / 16.0);
   p.cg = group_of(rows, (double)B * cdiv(rows, tile::kRows) * cdiv(cols, tile::kCols) * depth);
@@ -258,7 +267,8 @@ inline Plan plan_splits(int B, long long rows, long long cols, long long kdim, i
   p.runs = p.col_tiles;
   p.kblocks = (int)cdiv(kdim, tile::kK);
   p.pairs = pairs;
-  p.planes = planes;
+  p.planes_a = planes_a;
+  p.planes_b = planes_b;
   const long long kt = (long long)p.pairs * p.kblocks;
   double best = 1e30;
   p.ksplits = 1;

@@ -308,12 +308,12 @@ constexpr long long kGradBudget = 4LL << 30;  // bytes of G held at a time
 
 BwdSpace bwd_space(const Dims &m, bool bias, bool dbias, void *base) {
   BwdSpace f = {};
-  const long long row_bytes = m.Kp * 2 * m.planes;
+  const long long row_bytes = m.Kp * 2 * m.g_planes;
   f.nr = std::min<long long>(std::max<long long>(m.N, 1), std::max<long long>(256, kGradBudget / row_bytes / 256 * 256));
   f.bn = f.nr < m.N ? 1 : (int)std::max<long long>(1, std::min<long long>(m.B, kGradBudget / (row_bytes * f.nr)));
   f.pg = plan_runs(f.bn, f.nr, m.Kp, m.d, m.pairs, m.planes, m.dp * 2 * m.planes);
-  f.px = plan_splits(f.bn, f.nr, m.d, m.K, m.pairs, m.planes);
-  f.pw = plan_splits(f.bn, m.K, m.d, f.nr, m.pairs, m.planes);
+  f.px = plan_splits(f.bn, f.nr, m.d, m.K, m.g_pairs, m.g_planes, m.planes);
+  f.pw = plan_splits(f.bn, m.K, m.d, f.nr, m.g_pairs, m.g_planes, m.planes);
   f.w_parts = f.pw.ksplits > 1 || f.nr < m.N;
   Carve w(base);
   f.bound = (unsigned *)w.take(16);
@@ -368,7 +368,7 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
       ga.bound = bound;
       ga.nr = nr, ga.row_stride = m.N, ga.K = m.K, ga.Kp = m.Kp;
       ga.g = f.g;
-      ga.planes = m.planes;
+      ga.planes = m.g_planes;
       ga.colpart = dbias ? f.colpart : nullptr;
       ga.nblk = cdiv(nr, 32);
       // scores as exact as the forward pass's where fp32 results hang on them;
@@ -385,12 +385,12 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
       // dx = G C: the contraction is the table's rows
       if (dx) {
         CUtensorMap tg, tcm;
-        FK_TRY(map_16(&tg, f.g, bf, m.Kp, nr, (long long)bn * m.planes, m.Kp, nr * m.Kp, tile::kK, tile::kRows));
+        FK_TRY(map_16(&tg, f.g, bf, m.Kp, nr, (long long)bn * m.g_planes, m.Kp, nr * m.Kp, tile::kK, tile::kRows));
         FK_TRY(map_16(&tcm, (const char *)cmul + coff, bf, m.dp, m.K, (long long)bn * m.planes, m.dp,
                       (long long)m.K * m.dp, 64, tile::kK));
         Plan px = f.px;
         if (bn != f.bn || nr != f.nr) {
-          px = plan_splits(bn, nr, m.d, m.K, m.pairs, m.planes);
+          px = plan_splits(bn, nr, m.d, m.K, m.g_pairs, m.g_planes, m.planes);
           if (px.ksplits > f.px.ksplits || (long long)px.ksplits * bn * nr > (long long)f.px.ksplits * f.bn * f.nr) {
             px.ksplits = f.px.ksplits;
             px.units = (int)((long long)bn * px.row_tiles * px.runs * px.ksplits);
@@ -411,13 +411,13 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
       // dc = G^T X: the contraction is the rows
       if (dc) {
         CUtensorMap tg, txm;
-        FK_TRY(map_16(&tg, f.g, bf, m.Kp, nr, (long long)bn * m.planes, m.Kp, nr * m.Kp, 64, tile::kK));
+        FK_TRY(map_16(&tg, f.g, bf, m.Kp, nr, (long long)bn * m.g_planes, m.Kp, nr * m.Kp, 64, tile::kK));
         FK_TRY(map_16(&txm, (const char *)f.xs + xoff, bf, m.dp, nr, (long long)bn * m.planes, m.dp, m.N * m.dp, 64,
                       tile::kK));
         Plan pw = f.pw;
         if (bn != f.bn || nr != f.nr) {
           // the partial sums keep their slots over all blocks of rows
-          pw = plan_splits(bn, m.K, m.d, nr, m.pairs, m.planes);
+          pw = plan_splits(bn, m.K, m.d, nr, m.g_pairs, m.g_planes, m.planes);
           const long long kt = (long long)pw.pairs * pw.kblocks;
           pw.ksplits = (int)std::min<long long>(f.pw.ksplits, kt);
           pw.units = (int)((long long)bn * pw.row_tiles * pw.runs * pw.ksplits);

@@ -88,8 +88,8 @@ struct Plan {
   int ksplits;      // parts of the contraction
   int group;        // row tiles per group
   int kblocks;      // 64-wide blocks of one plane pair
-  int pairs;        // 1, or 6 for fp32
-  int planes;       // 1, or 3
+  int pairs;        // of planes: 1, 2 (A in two parts), or 6 for fp32
+  int planes_a, planes_b;  // 1, 2 or 3
   int stages;
   uint32_t idesc;
 };
@@ -121,8 +121,9 @@ __host__ __device__ __forceinline__ Unit unit_of(const Plan &p, int u) {
 
 // The plane pair of a contraction step, smallest products first.
 __device__ __forceinline__ void pair_planes(int pairs, int pair, int &pa, int &pb) {
-  if (pairs == 1) {
-    pa = pb = 0;
+  if (pairs < 6) {
+    pa = pairs - 1 - pair;
+    pb = 0;
     return;
   }
   // (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
@@ -315,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           int pair = w.k0 / p.kblocks, kb = w.k0 - pair * p.kblocks;
           int pa, pb;
           pair_planes(p.pairs, pair, pa, pb);
-          pa += w.b * p.planes;
-          pb += w.b * p.planes;
+          pa += w.b * p.planes_a;
+          pb += w.b * p.planes_b;
           for (int k = w.k0; k < w.k1; ++k, ++it) {
             if (!mbar_wait_spin(empty(s), ph, abort_flag, err)) { ok = false; break; }
             const uint32_t sa = base + s * G::kStageBytes, sb = sa + kABytes;
@@ -340,8 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               kb = 0;
               if (++pair < p.pairs) {
                 pair_planes(p.pairs, pair, pa, pb);
-                pa += w.b * p.planes;
-                pb += w.b * p.planes;
+                pa += w.b * p.planes_a;
+                pb += w.b * p.planes_b;
               }
             }
             if (++s == p.stages) {
