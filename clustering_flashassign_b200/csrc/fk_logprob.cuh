@@ -272,7 +272,7 @@ inline Plan plan_splits(int B, long long rows, long long cols, long long kdim, i
   const long long kt = (long long)p.pairs * p.kblocks;
   double best = 1e30;
   p.ksplits = 1;
-  for (int ks = 1; ks <= 16 && ks <= kt; ++ks) {
+  for (int ks = 1; ks <= 64 && ks <= kt; ++ks) {
     const double t = (double)cdiv((long long)B * p.row_tiles * p.runs * ks, workers) *
                      ((double)cdiv(kt, ks) + 4.0 + (ks > 1 ? 8.0 : 0.0));
     if (t < best * 0.98) {
