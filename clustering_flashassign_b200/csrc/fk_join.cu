@@ -31,7 +31,7 @@ __device__ __forceinline__ void exact_scores(const T *x, const T *c, const float
   for (int i = 0; i < C; ++i) s[i] = 0.0;
   constexpr int V = 16 / sizeof(T);
   if (vec) {
-#pragma unroll(C == 1 ? 4 : 2)
+#pragma unroll(C <= 2 ? 4 : 2)
     for (int j = lane; j < d / V; j += LPR) {
       T xv[V], cv[C][V];
       *reinterpret_cast<uint4 *>(xv) = __ldg(reinterpret_cast<const uint4 *>(x) + j);
@@ -446,7 +446,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a
     const int other = j + kJoinWarps < a.cands ? j + kJoinWarps : j;
     const int k[2] = {cand[j], cand[other]};
     double e[2];
-    exact_scores<T, 32, 2>(x, c, bias, a.scale, k, a.d, a.vec, lane, e);
+    if (other == j) {
+      const int k1[1] = {k[0]};
+      double e1[1];
+      exact_scores<T, 32, 1>(x, c, bias, a.scale, k1, a.d, a.vec, lane, e1);
+      e[0] = e1[0];
+    } else {
+      exact_scores<T, 32, 2>(x, c, bias, a.scale, k, a.d, a.vec, lane, e);
+    }
     if (lane == 0) {
       exact[j] = e[0];
       if (other != j) exact[other] = e[1];

@@ -100,6 +100,8 @@ def token_log_probs(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, *, scal
     negative: ignored (log probability 0, no gradient from it).  bias (K,) or (B, K);
     -inf masks an entry.  top <= min(K, 28) likeliest entries, lowest index on ties.
     logp, lse and entropy are fp32 and differentiable; top_ids and top_logp are not.
+    The backward pass can be captured into a CUDA graph while no eager autograd graph of
+    the same leaves is alive; fk_logprob and fk_logprob_backward can be captured always.
     """
     if x.dim() < 1 or c.dim() not in (2, 3) or (c.dim() == 3 and x.dim() != 3):
         raise ValueError("x must be (..., d) and c (K, d), or x (B, N, d) and c (B, K, d)")
