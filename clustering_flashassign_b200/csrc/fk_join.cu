@@ -132,6 +132,7 @@ __device__ __forceinline__ void insert_ordered(float (&hv)[LL], int (&hk)[LL], f
 // probability is a small difference of small numbers.
 struct RowStat {
   float m, ls, hs;  // hs = (sum e (t - m)) / sum
+  float sig;        // the sum's significand, 2^ls
   bool none;        // every column is masked: lse = -inf, entropy 0
   bool nan;
 };
@@ -144,19 +145,26 @@ __device__ __forceinline__ RowStat row_stat(float m, float s, float u) {
   if (s > 0.f && s < INFINITY) {
     const int e = ilogbf(s);
     r.m = m + (float)e;
-    r.ls = log2f(scalbnf(s, -e));
+    r.sig = scalbnf(s, -e);
+    r.ls = log2f(r.sig);
     r.hs -= (float)e;
   } else {
     r.m = m;
+    r.sig = s;
     r.ls = log2f(s);
   }
   return r;
 }
 
-// Log probability of a stored score (a product, or in base 2 with a bias).
+// Log probability of a stored score (a product, or in base 2 with a bias).  Of
+// a column that holds more than half of the sum it is -log1p(what the others
+// add / e): the sum has the same ex2.approx of the same score in it, whose error
+// (2^-22 of it) cancels in the difference instead of standing beside a small result.
 __device__ __forceinline__ float stored_logp(const JoinArgs &a, const RowStat &q, float v) {
   if (q.none || (v == kNegInf && !q.nan)) return kNegInf;
   const float rel = a.bias ? v - q.m : fmaf(v, a.scale * kLog2e, -q.m);
+  const float e = ex2(rel);
+  if (e + e > q.sig && q.sig < INFINITY) return -log1pf(fmaxf(q.sig - e, 0.f) / e);
   return -at_least_0((q.ls - rel) * kLn2);
 }
 
