@@ -165,8 +165,7 @@ struct StatArgs {
   int32_t *top_i;
 };
 
-// Joins a row's partial results (one warp per row).
-// Up to this many rows, a row whose alternatives are asked for gets a block.
+// Up to this many rows, a row whose alternatives are asked for gets a block in the join.
 constexpr long long kJoinBlockRows = 4096;
 
 struct JoinArgs {
@@ -225,7 +224,6 @@ inline int check_soft(const fk_shape *shape, float scale) {
   if (!(scale > 0.f) || !(scale < INFINITY)) return set_error(FK_EINVAL, "scale must be positive and finite");
   return FK_OK;
 }
-
 
 // Row tiles x column runs over the workers: the fewest rounds of units, with
 // the start and the partial results of a unit counted as a quarter of a tile.
@@ -299,7 +297,6 @@ int launch_group(const CUtensorMap &ta, const CUtensorMap &tb, Plan p, const typ
   constexpr uint32_t stage = tile::Geo<kCG>::kStageBytes;
   const size_t cap = 227 * 1024 - 1024 - tile::kCtrlBytes;
   p.stages = (int)std::min<size_t>(tile::kMaxStages, (cap - epi_smem) / stage);
-  
   p.idesc = sm100::idesc_f32acc((uint32_t)ab_fmt, tile::kRows * kCG, tile::kCols) | (A_MN ? 1u << 15 : 0u) |
             (B_MN ? 1u << 16 : 0u);
   const int smem = (int)(1024 + p.stages * stage + tile::kCtrlBytes + epi_smem);
