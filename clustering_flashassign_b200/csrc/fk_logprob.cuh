@@ -380,20 +380,41 @@ __device__ __forceinline__ void copy_row(const T *src, long long r, long long ro
     const long long b = r / rows_per_b;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(dst) + ((size_t)(b * 3) * rows_per_b + (r - b * rows_per_b)) * dp;
     const size_t plane = (size_t)rows_per_b * dp;
-    for (int j = 2 * lane; j < dp; j += 64) {
-      float v[2];
+    // four values a lane, eight loads of a row in flight (N 573, K 123, d 3969:
+    // 10 us a copy against 38 with one at a time)
+    constexpr int U = 8;
+    const bool vec = d % 4 == 0 && (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+    for (int j0 = 4 * lane; j0 < dp; j0 += 128 * U) {
+      float v[U][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) v[i] = j + i < d && !drop ? in[j + i] : 0.f;
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + 128 * u;
+        if (vec) {
+          const float4 w = j < d && !drop ? __ldg(reinterpret_cast<const float4 *>(in + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[u][0] = w.x, v[u][1] = w.y, v[u][2] = w.z, v[u][3] = w.w;
+        } else {
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        __nv_bfloat162 h;
-        h.x = __float2bfloat16_rn(v[0]);
-        h.y = __float2bfloat16_rn(v[1]);
-        *reinterpret_cast<__nv_bfloat162 *>(out + p * plane + j) = h;
-        const float2 f = __bfloat1622float2(h);
-        // an infinity (or an overflow of the rounding) leaves no remainder
-        v[0] = fabsf(f.x) < INFINITY ? v[0] - f.x : 0.f;
-        v[1] = fabsf(f.y) < INFINITY ? v[1] - f.y : 0.f;
+          for (int i = 0; i < 4; ++i) v[u][i] = j + i < d && !drop ? __ldg(in + j + i) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + 128 * u;
+        if (j >= dp) break;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          __nv_bfloat162 h[2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat16 t = __float2bfloat16_rn(v[u][i]);
+            const float f = __bfloat162float(t);
+            // an infinity (or an overflow of the rounding) leaves no remainder
+            v[u][i] = fabsf(f) < INFINITY ? v[u][i] - f : 0.f;
+            if (i & 1) h[i / 2].y = t;
+            else h[i / 2].x = t;
+          }
+          *reinterpret_cast<uint2 *>(out + p * plane + j) = *reinterpret_cast<const uint2 *>(h);
+        }
       }
     }
   }
