@@ -59,6 +59,13 @@ inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 // tiles: 69 us against 63 by pairs).
 inline int group_of(long long rows, double tiles) { return rows <= tile::kRows || tiles < 2.0 * num_sms() ? 1 : 2; }
 
+// Few tiles of a deep contraction take pairs too, if all find room at once: a
+// tile's time is then that of its copies, whose rows the copy unit takes one by
+// one, 384 a K-block by one CTA and 256 by a pair (fp32, N 92, K 326, d 3250, 306
+// K-blocks: 140 us against 186; at 48 to 64 K-blocks 2 to 4 us slower, since pairs
+// start later).
+constexpr int kDeepBlocks = 128;
+
 __device__ __forceinline__ float ex2(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -230,10 +237,13 @@ inline int check_soft(const fk_shape *shape, float scale) {
 inline Plan plan_runs(int B, long long rows, long long cols, int kdim, int pairs, int planes, int row_bytes) {
   Plan p = {};
   p.cg = group_of(rows, (double)B * cdiv(rows, tile::kRows) * cdiv(cols, tile::kCols));
+  p.kblocks = (int)cdiv(kdim, tile::kK);
+  if (p.kblocks * pairs >= kDeepBlocks &&
+      2.0 * B * cdiv(rows, 2 * tile::kRows) * cdiv(cols, tile::kCols) <= num_sms())
+    p.cg = 2;
   const int workers = num_sms() / p.cg;
   p.row_tiles = (int)cdiv(rows, tile::kRows * p.cg);
   p.col_tiles = (int)cdiv(cols, tile::kCols);
-  p.kblocks = (int)cdiv(kdim, tile::kK);
   p.pairs = pairs;
   p.planes_a = p.planes_b = planes;
   p.ksplits = 1;
