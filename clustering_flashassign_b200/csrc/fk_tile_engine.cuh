@@ -21,7 +21,7 @@
 //
 // fp32 operands come as three bf16 planes (hi, mid, lo: 8 + 8 + 8 significant
 // bits) and the contraction runs over the six plane pairs whose product is
-// above 2^-24 of the leading one, smallest first.  That costs 6 bf16 products,
+// above 2^-24 of the leading one, smallest of a segment first.  That costs 6 bf16 products,
 // exactly the tensor time of three TF32 ones at half the rate, keeps fp32's
 // range, and needs no second set of layouts (TF32 operands cannot be read
 // MN-major).
@@ -119,7 +119,7 @@ __host__ __device__ __forceinline__ Unit unit_of(const Plan &p, int u) {
   return w;
 }
 
-// The plane pair of a contraction step, smallest products first.
+// The plane pair of a contraction step, smallest products of a group of K-blocks first.
 __device__ __forceinline__ void pair_planes(int pairs, int pair, int &pa, int &pb) {
   if (pairs < 6) {
     pa = pairs - 1 - pair;
@@ -313,7 +313,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int arow = (w.rt * CG + (int)rank) * kRows;
         for (int ct = w.ct0; ct < w.ct1 && ok; ++ct) {
           const int bcol = ct * kCols + (int)rank * (kCols / CG);
-          int pair = w.k0 / p.kblocks, kb = w.k0 - pair * p.kblocks;
+          // kSegBlocks K-blocks of every plane pair, then the next kSegBlocks: a
+          // plane is read again while it is in L2 (fp32 training, N 14, K 61507,
+          // d 2670: 1890 us against 1970 with a pair's whole contraction at a time)
+          int g0 = w.k0 / (kSegBlocks * p.pairs);
+          const int at = w.k0 - g0 * (kSegBlocks * p.pairs);
+          g0 *= kSegBlocks;
+          int gend = min(g0 + kSegBlocks, p.kblocks), pair = at / (gend - g0), kb = g0 + at - pair * (gend - g0);
           int pa, pb;
           pair_planes(p.pairs, pair, pa, pb);
           pa += w.b * p.planes_a;
@@ -337,13 +343,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               load_3d<CG>(&tb, sb, bar, kb * kK, bcol, pb);
             }
-            if (++kb == p.kblocks) {
-              kb = 0;
-              if (++pair < p.pairs) {
-                pair_planes(p.pairs, pair, pa, pb);
-                pa += w.b * p.planes_a;
-                pb += w.b * p.planes_b;
+            if (++kb == gend) {
+              if (++pair == p.pairs) {
+                pair = 0;
+                g0 = gend;
+                gend = min(g0 + kSegBlocks, p.kblocks);
               }
+              kb = g0;
+              pair_planes(p.pairs, pair, pa, pb);
+              pa += w.b * p.planes_a;
+              pb += w.b * p.planes_b;
             }
             if (++s == p.stages) {
               s = 0;
