@@ -38,9 +38,14 @@
 // columns sums its slots in order, so results do not depend on the order of
 // arrival.
 //
-// h is held as hi + lo of the weights' type (bf16: 16 significant bits; fp16:
-// 22, of h / 64 to keep the type's range ahead of h), so that rounding it does
-// not add to the result's own rounding.
+// h is held in two parts of the weights' type, so that rounding it does not add
+// to the result's own rounding: hi + lo in bf16 (16 significant bits), and in
+// fp16 h / 64 = hi + lo / 2^11 (22 bits).  The division keeps the type's range
+// ahead of h (|h| up to 4.19e6; beyond, h counts as infinite), and what hi
+// leaves is at most 2^-11 of it, so lo at 2^11 times its size fits and stays off
+// the type's lower end: small h are off by 2^-30 at most (unscaled, 2^-19: 1% of
+// the result where gate and up products are near 0.01).  lo's products are
+// summed on their own and join with the factor 2^-11.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -61,7 +66,8 @@ constexpr int kMaxTopK = 16;
 constexpr int kRouteCtas = 8;  // CTAs of a cluster
 constexpr int kRouteTokens = 4;  // its tokens
 constexpr int kWarps = 8;
-constexpr float kHalfScale = 1.f / 64.f;
+constexpr float kHalfScale = 1.f / 64.f;  // fp16: of h
+constexpr float kLowScale = 2048.f;       // fp16: of what hi leaves of h
 
 struct MoeArgs {
   int T, E, d, F, k, act, renorm;
@@ -279,14 +285,16 @@ __device__ __forceinline__ int load_acquire(const int *p) {
 }
 
 // c[n] += rows (lo row, hi row of this lane) x tokens over the 32-element
-// steps sub, sub + S, ... of a group of S warps.  SPLIT: the tokens' side is hi + lo.
+// steps sub, sub + S, ... of a group of S warps.  SPLIT: the tokens' side is in two parts.
 template <typename T, int NT, bool SPLIT>
 __device__ __forceinline__ void contract(float (&c)[NT][4], const T *r0, const T *r1, const T *const (&tok)[NT],
                                          const T *const (&tok2)[NT], int len, int sub, int S, int q) {
   constexpr int U = NT == 1 ? (SPLIT ? 4 : 6) : NT == 2 ? 3 : 2;  // steps in flight
   constexpr bool BF = Two<T>::kBf;
+  constexpr bool APART = SPLIT && !BF;  // the second part has a scale of its own
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const int step = 32 * S;
+  float low[APART ? NT : 1][4] = {};
   for (int k0 = sub * 32 + q * 8; k0 < len + q * 8; k0 += step * U) {
     uint4 A0[U], A1[U];
 #pragma unroll
@@ -317,11 +325,18 @@ __device__ __forceinline__ void contract(float (&c)[NT][4], const T *r0, const T
         mma16816<BF>(c[n], A0[u].x, A1[u].x, A0[u].y, A1[u].y, B[u][n].x, B[u][n].y);
         mma16816<BF>(c[n], A0[u].z, A1[u].z, A0[u].w, A1[u].w, B[u][n].z, B[u][n].w);
         if (SPLIT) {
-          mma16816<BF>(c[n], A0[u].x, A1[u].x, A0[u].y, A1[u].y, B2[u][n].x, B2[u][n].y);
-          mma16816<BF>(c[n], A0[u].z, A1[u].z, A0[u].w, A1[u].w, B2[u][n].z, B2[u][n].w);
+          float(&c2)[4] = APART ? low[APART ? n : 0] : c[n];
+          mma16816<BF>(c2, A0[u].x, A1[u].x, A0[u].y, A1[u].y, B2[u][n].x, B2[u][n].y);
+          mma16816<BF>(c2, A0[u].z, A1[u].z, A0[u].w, A1[u].w, B2[u][n].z, B2[u][n].w);
         }
       }
     }
+  }
+  if constexpr (APART) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[n][i] = fmaf(low[n][i], 1.f / kLowScale, c[n][i]);
   }
 }
 
@@ -429,8 +444,9 @@ __device__ __forceinline__ void unit_pass(const MoeArgs &a, ExpertSmem &sm, cons
           if (!BF) h *= kHalfScale;
           const size_t at = (size_t)slot * a.F + row0 + g;
           const T hi = static_cast<T>(h);
+          const float left = fabsf(static_cast<float>(hi)) < INFINITY ? h - static_cast<float>(hi) : 0.f;
           static_cast<T *>(a.hi)[at] = hi;
-          static_cast<T *>(a.lo)[at] = static_cast<T>(h - static_cast<float>(hi));
+          static_cast<T *>(a.lo)[at] = static_cast<T>(BF ? left : left * kLowScale);
         }
       }
     }

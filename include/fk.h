@@ -371,7 +371,8 @@ int fk_logprob_backward_workspace(const fk_shape *shape, int with_bias, int with
  * x (T, d), router (E, d), w_in (E, 2F, d): an expert's F gate rows, then its F
  * up rows; w_out (E, d, F); y (T, d); expert_ids, expert_weights (T, top_k) int32
  * / fp32, largest first.  fp16 or bf16 throughout (fp32: FK_EUNSUPPORTED), sums
- * in fp32, scores in fp64.  Only the chosen experts' weights are read.
+ * in fp32, scores in fp64.  Only the chosen experts' weights are read.  In fp16,
+ * |h| beyond 4.19e6 counts as infinite.
  * Limits: 0 <= T <= 256, E <= 512, top_k <= min(E, 16), d and F multiples of 8.
  * A NaN score ranks last; a token with one gets NaN weights and a NaN row of y
  * and leaves the other tokens as they are.  Tensors 16-byte aligned (y, ids and
