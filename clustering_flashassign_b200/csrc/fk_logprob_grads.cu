@@ -407,9 +407,10 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
       ga.planes = m.g_planes;
       ga.colpart = dbias ? f.colpart : nullptr;
       ga.nblk = cdiv(nr, 32);
-      // scores as exact as the forward pass's where fp32 results hang on them;
-      // a 16-bit gradient does not show the difference (2^-15 against 2^-9)
-      if ((m.planes == 3 || dbias) && pg.kblocks * pg.pairs > tile::kSegBlocks)
+      // the forward pass's scores, summed in the same segments: p is normalised by
+      // their lse, and of a confident row's 1 - p a difference of 1e-4 would be all
+      // that is seen (one chain of 2048 terms: 3e-6 of the score)
+      if (pg.kblocks * pg.pairs > tile::kSegBlocks)
         FK_TRY((launch_tiles<GradEpi<G, BIAS, true>, false, false>(tx, tc, pg, ga, GradEpi<G, BIAS, true>::smem_bytes(), fmt, err, s)));
       else
         FK_TRY((launch_tiles<GradEpi<G, BIAS, false>, false, false>(tx, tc, pg, ga, GradEpi<G, BIAS, false>::smem_bytes(), fmt, err, s)));
