@@ -129,10 +129,11 @@ __device__ __forceinline__ void insert_ordered(float (&hv)[LL], int (&hk)[LL], f
 
 // A row's joined statistics: lse = m + ls in base 2 with m whole and ls in [0, 1)
 // (ls = log2 of the sum's significand), so that a confident row's log
-// probability is a small difference of small numbers.
+// probability is a small difference of small numbers.  An m of 2^23 or more in
+// magnitude cannot take in the sum's exponent: ls is then log2 of the whole sum.
 struct RowStat {
   float m, ls, hs;  // hs = (sum e (t - m)) / sum
-  float sig;        // the sum's significand, 2^ls
+  float sig;        // 2^ls
   bool none;        // every column is masked: lse = -inf, entropy 0
   bool nan;
 };
@@ -142,7 +143,7 @@ __device__ __forceinline__ RowStat row_stat(float m, float s, float u) {
   r.none = m == kNegInf && s == 0.f;
   r.nan = !(s == s);
   r.hs = u / s;
-  if (s > 0.f && s < INFINITY) {
+  if (s > 0.f && s < INFINITY && fabsf(m) < 8388608.f) {
     const int e = ilogbf(s);
     r.m = m + (float)e;
     r.sig = scalbnf(s, -e);
