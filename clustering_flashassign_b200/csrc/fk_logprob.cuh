@@ -94,6 +94,15 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
+// A finite bias beyond 2^31 in magnitude counts as that: the lowest values of
+// bf16 and fp32, which programs mask with, would overflow times log2 e, and
+// 0 * inf is NaN.  What is masked so adds exactly nothing beside an ordinary
+// column, and lse and its rest still hold a row of nothing else (2^-16).
+constexpr float kMaxBias = 2147483648.f;
+__device__ __forceinline__ float clamp_bias(float b) {
+  return fabsf(b) > kMaxBias && fabsf(b) < INFINITY ? copysignf(kMaxBias, b) : b;
+}
+
 // A warp's bias of its (at most four) 32-column chunks of a tile, times log2 e,
 // in shared memory; columns past the last count as masked.  `masked`: which of
 // the chunks hold a masked column.
@@ -108,7 +117,7 @@ struct BiasTile {
     for (int i = 0; i < 4; ++i) {
       const long long col = col0 + i * stride + lane;
       const float b = col < K ? __ldg(bias + col) : kNegInf;
-      sb[i * 32 + lane] = b * kLog2e;
+      sb[i * 32 + lane] = clamp_bias(b) * kLog2e;
       if (__any_sync(0xffffffffu, b == kNegInf)) masked |= 1u << i;
     }
     __syncwarp();

@@ -98,7 +98,7 @@ def token_log_probs(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, *, scal
     x (..., d) with one table c (K, d) and ids (...), or batches x (B, N, d), c (B, K, d),
     ids (B, N); fp16, bf16 (d a multiple of 8) or fp32, x and c alike.  ids int32 or int64,
     negative: ignored (log probability 0, no gradient from it).  bias (K,) or (B, K);
-    -inf masks an entry.  top <= min(K, 28) likeliest entries, lowest index on ties.
+    -inf masks an entry; a finite bias beyond 2^31 in magnitude counts as +-2^31.  top <= min(K, 28) likeliest entries, lowest index on ties.
     logp, lse and entropy are fp32 and differentiable; top_ids and top_logp are not.
     The backward pass can be captured into a CUDA graph while no eager autograd graph of
     the same leaves is alive; fk_logprob and fk_logprob_backward can be captured always.

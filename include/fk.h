@@ -326,11 +326,14 @@ int fk_noalloc_device_error(fk_stream_t stream);
  *
  * shape: N >= 0 (K may exceed N), d <= 2^20, otherwise fk_assign's rules.
  * scale positive and finite.  bias fp32 (B, K), nullable; an entry of -inf masks
- * its column whatever the table's row holds.  0 <= top <= min(K, 28).  A negative
- * id is ignored: its logp is 0.  An id of K or more does the same and records
- * FK_EINVAL in the device error word.  A row whose every column is masked has
- * lse = logp = -inf and entropy 0; masked columns fill up top, lowest index
- * first.  fp32 inputs are multiplied as three bf16 parts each (about 2^-24).
+ * its column whatever the table's row holds.  A finite bias beyond 2^31 in
+ * magnitude counts as +-2^31: the lowest values of bf16 and fp32 leave nothing of
+ * a column beside an ordinary one, and rows of nothing else stay finite.
+ * 0 <= top <= min(K, 28).  A negative id is ignored: its logp is 0.  An id of K or
+ * more does the same and records FK_EINVAL in the device error word.  A row whose
+ * every column is masked has lse = logp = -inf and entropy 0; masked columns fill
+ * up top, lowest index first.  fp32 inputs are multiplied as three bf16 parts each
+ * (about 2^-24).
  *
  * workspace: device memory of the caller's (16-byte aligned, at least
  * fk_logprob_workspace bytes), in use until the call's work on `stream` is
