@@ -1,4 +1,9 @@
 // Joins the partial results of the score kernels, row by row.
+//
+// These kernels are resident while the score kernel still writes its partial
+// results (it triggers its dependents at its start): what it writes is read with
+// ordinary loads after pdl_wait(), never through the read-only path.  x, c and
+// bias are older than the score kernel, and finished.
 #include "fk_logprob.cuh"
 
 namespace fk {
@@ -253,9 +258,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const JoinArgs a) {
     const int32_t *pk = a.top_i + (r * a.parts + p) * a.L;
 #pragma unroll 1
     for (int j = 0; j < LL; ++j) {
-      const int k = __ldg(pk + j);
+      const int k = pk[j];
       if (k < 0) break;
-      insert_ordered<LL>(hv, hk, __ldg(pv + j), k);
+      insert_ordered<LL>(hv, hk, pv[j], k);
     }
   }
   __syncwarp();
@@ -370,9 +375,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a
   float m = kNegInf, s = 0.f, u = 0.f, tgt = kNegInf;
   unsigned long long head = 0ull;
   for (int p = tid; p < a.parts; p += 32 * kJoinWarps) {
-    const float4 q = __ldg(a.part + r * a.parts + p);
+    const float4 q = a.part[r * a.parts + p];
     const long long o = (r * a.parts + p) * a.L;
-    head = max(head, column_key(__ldg(a.top_v + o), __ldg(a.top_i + o)));
+    head = max(head, column_key(a.top_v[o], a.top_i[o]));
     join_stats(m, s, u, q.x, q.y, q.z);
     tgt = fmaxf(tgt, q.w);
   }
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a
       const long long o = (r * a.parts + p) * a.L;
 #pragma unroll 1
       for (int j = 0; j < a.L; ++j) {  // sorted: the rest is lower
-        const unsigned long long key = column_key(__ldg(a.top_v + o + j), __ldg(a.top_i + o + j));
+        const unsigned long long key = column_key(a.top_v[o + j], a.top_i[o + j]);
         if (!key || key < least) break;
         found[atomicAdd(&n_found, 1)] = key;
       }
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(256) k_join_rows(const JoinArgs a) {
   const long long r = live ? r0 : a.rows - 1, b = r / a.N;
   float m = kNegInf, s = 0.f, u = 0.f, tgt = kNegInf;
   for (int p = 0; p < a.parts; ++p) {
-    const float4 q = __ldg(a.part + r * a.parts + p);
+    const float4 q = a.part[r * a.parts + p];
     join_stats(m, s, u, q.x, q.y, q.z);
     tgt = fmaxf(tgt, q.w);
   }
@@ -512,8 +517,8 @@ __global__ void __launch_bounds__(256) k_join_rows(const JoinArgs a) {
     const int4 *pk = reinterpret_cast<const int4 *>(a.top_i + (r * a.parts + p) * a.L);
 #pragma unroll
     for (int q = 0; q < C / 4; ++q) {
-      const float4 v4 = __ldg(pv + q);
-      const int4 k4 = __ldg(pk + q);
+      const float4 v4 = pv[q];
+      const int4 k4 = pk[q];
       const float nv[4] = {v4.x, v4.y, v4.z, v4.w};
       const int nk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll

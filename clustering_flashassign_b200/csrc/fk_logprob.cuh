@@ -116,7 +116,7 @@ struct BiasTile {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const long long col = col0 + i * stride + lane;
-      const float b = col < K ? __ldg(bias + col) : kNegInf;
+      const float b = col < K ? bias[col] : kNegInf;
       sb[i * 32 + lane] = clamp_bias(b) * kLog2e;
       if (__any_sync(0xffffffffu, b == kNegInf)) masked |= 1u << i;
     }
@@ -386,15 +386,27 @@ struct FwdSpace {
 // bf16 planes of dp >= d elements (zero padded).  drop: rows whose gradient is
 // zero whatever they hold (padding), or table rows that a bias of -inf masks,
 // become zero, so that what they hold (NaN included) stays out of the products.
+// The kernel before may still have been writing src when this one became
+// resident: ordinary loads.
 template <typename T>
 __device__ __forceinline__ void copy_row(const T *src, long long r, long long rows_per_b, int d, int dp, bool drop,
                                          void *dst, int lane) {
   const T *in = src + (size_t)r * d;
   if constexpr (sizeof(T) == 2) {
     uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(dst) + (size_t)r * d);
-#pragma unroll 4
-    for (int j = lane; j < d / 8; j += 32)
-      out[j] = drop ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(in) + j);
+    const uint4 *in16 = reinterpret_cast<const uint4 *>(in);
+    constexpr int U = 4;  // loads in flight
+    for (int j0 = lane; j0 < d / 8; j0 += 32 * U) {
+      uint4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v[u] = make_uint4(0, 0, 0, 0);
+        if (j0 + 32 * u < d / 8 && !drop) v[u] = in16[j0 + 32 * u];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (j0 + 32 * u < d / 8) out[j0 + 32 * u] = v[u];
+    }
   } else {
     const long long b = r / rows_per_b;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(dst) + ((size_t)(b * 3) * rows_per_b + (r - b * rows_per_b)) * dp;
@@ -409,11 +421,11 @@ __device__ __forceinline__ void copy_row(const T *src, long long r, long long ro
       for (int u = 0; u < U; ++u) {
         const int j = j0 + 128 * u;
         if (vec) {
-          const float4 w = j < d && !drop ? __ldg(reinterpret_cast<const float4 *>(in + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 w = j < d && !drop ? *reinterpret_cast<const float4 *>(in + j) : make_float4(0.f, 0.f, 0.f, 0.f);
           v[u][0] = w.x, v[u][1] = w.y, v[u][2] = w.z, v[u][3] = w.w;
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[u][i] = j + i < d && !drop ? __ldg(in + j + i) : 0.f;
+          for (int i = 0; i < 4; ++i) v[u][i] = j + i < d && !drop ? in[j + i] : 0.f;
         }
       }
 #pragma unroll

@@ -136,7 +136,7 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(32 * kWarps
     for (int t = 0; t < kRouteTokens; ++t) {
       if (t < nt) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (k < a.d) v = __ldg(reinterpret_cast<const uint4 *>(xs + (size_t)t * a.d + k));
+        if (k < a.d) v = *reinterpret_cast<const uint4 *>(xs + (size_t)t * a.d + k);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -152,7 +152,7 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(32 * kWarps
       for (int i = 0; i < kRouteBatch; ++i) {
         r[i] = make_uint4(0, 0, 0, 0);
         if (e0 + i < mine && k < a.d)
-          r[i] = __ldg(reinterpret_cast<const uint4 *>(rs + (size_t)(cta + (e0 + i) * kRouteCtas) * a.d + k));
+          r[i] = *reinterpret_cast<const uint4 *>(rs + (size_t)(cta + (e0 + i) * kRouteCtas) * a.d + k);
       }
     };
     fetch(0);

@@ -57,7 +57,7 @@ struct StatEpi {
     row = row0 + r;
     idle = row0 + (r & ~31) >= a.N;
     at = w.b * a.N + row;
-    id = row < a.N ? __ldg(a.ids + at) : -1;
+    id = row < a.N ? a.ids[at] : -1;
     if (BIAS) bias = a.bias + w.b * a.K;
     m = thr = tgt = kNegInf;
     sum = us = 0.f;
