@@ -362,7 +362,11 @@ struct Group {
   }
   // every thread of the group gets the leader's value
   __device__ __forceinline__ int share(ExpertSmem &sm, int v) const {
-    if (S == 1) return __shfl_sync(0xffffffffu, v, 0);
+    if (S == 1) {
+      v = __shfl_sync(0xffffffffu, v, 0);
+      __syncwarp();  // the exchange orders no memory: what the leader has seen, the others see from here on
+      return v;
+    }
     if (leader()) sm.word[id] = v;
     sync();
     const int r = *(volatile int *)&sm.word[id];

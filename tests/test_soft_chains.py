@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import clustering_flashassign_b200 as fk
+from clustering_flashassign_b200.soft import expert_mixture, token_log_probs
 
 pytestmark = pytest.mark.gpu
 
@@ -44,4 +45,39 @@ def test_assign_log_probabilities_and_gradients(N, K, d, dtype):
         got = [step(i, False) for i in range(4)]
         for w, v in zip(want, got):
             assert all(torch.equal(a, b) for a, b in zip(w, v))
+    assert fk.fk_device_error() == fk.FK_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k,d,F", [(1, 16, 2, 512, 256), (5, 64, 4, 264, 136), (200, 8, 2, 128, 512),
+                                       (64, 128, 8, 256, 96)])
+def test_layers_of_experts(T, E, k, d, F, dtype):
+    """Units of one warp and of several; every layer reads the one before.  (A layer squares
+    the size of its rows, times 3 / sqrt(2): three layers reach 100, five leave fp16's range.)"""
+    g = torch.Generator(device="cuda").manual_seed(T)
+
+    def normal(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+
+    layers = [((normal(E, d) / d ** 0.5).to(dtype), (normal(E, 2 * F, d) / d ** 0.5).to(dtype),
+               (normal(E, d, F) * 3 / F ** 0.5).to(dtype)) for _ in range(3)]
+    x = normal(T, d).to(dtype)
+
+    def run(wait):
+        out, h = [], x
+        for w in layers:
+            r = expert_mixture(h, *w, k)
+            if wait:
+                torch.cuda.synchronize()
+            h = r.y
+            out += list(r)
+            out += list(token_log_probs(h, w[0], r.expert_ids[:, 0], top=2))
+            if wait:
+                torch.cuda.synchronize()
+        return out
+
+    want = run(True)
+    assert torch.isfinite(want[-1]).all()
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(want, run(False)))
     assert fk.fk_device_error() == fk.FK_OK
