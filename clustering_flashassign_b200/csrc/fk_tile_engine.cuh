@@ -242,7 +242,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
                                           int lane) {
   int ok = 1;
   if (lane == 0) ok = mbar_wait_spin(bar, parity, abort_flag, err);
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();  // the exchange orders no memory: the wait does, and this hands it on
+  return ok != 0;
 }
 
 // What an epilogue sees.  Epi provides
