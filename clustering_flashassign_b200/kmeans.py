@@ -137,7 +137,8 @@ class FlashKMeans:
     def log_prob(self, data: torch.Tensor, ids: torch.Tensor | None = None, temperature: float = 1.0,
                  top: int = 0):
         """Soft assignment: log probabilities under softmax_k(-|x - c_k|^2 / temperature) of the
-        trained centroids.  ids: the clusters asked for (default: the nearest one, predict()).
+        trained centroids.  ids: the clusters asked for (default: the nearest one: predict(), or for
+        fewer rows than centroids, which predict() refuses, the likeliest one).
         Returns soft.TokenLogProbs: logp of ids, entropy of the assignment, the `top` likeliest
         clusters; lse omits -|x|^2 / temperature, which all clusters of a row share."""
         from .soft import token_log_probs
@@ -148,12 +149,16 @@ class FlashKMeans:
         x, squeeze = self._prep(data)
         if not x.is_cuda:
             x = x.to(self.device)
-        if ids is None:
-            ids = self.predict(data)
         c = (self.centroids.unsqueeze(0) if squeeze else self.centroids).to(self.dtype).contiguous()
         bias = c.float().square().sum(-1) * (-1.0 / temperature)
-        r = token_log_probs(x, c, (ids.unsqueeze(0) if squeeze else ids).to(x.device), scale=2.0 / temperature,
-                            bias=bias, top=top)
+        if ids is None and x.shape[1] < self.k:
+            none = torch.full(x.shape[:2], -1, dtype=torch.int32, device=x.device)
+            with torch.no_grad():
+                ids = token_log_probs(x, c, none, scale=2.0 / temperature, bias=bias, top=1).top_ids[..., 0]
+        else:
+            ids = self.predict(data) if ids is None else ids
+            ids = (ids.unsqueeze(0) if squeeze else ids).to(x.device)
+        r = token_log_probs(x, c, ids, scale=2.0 / temperature, bias=bias, top=top)
         return type(r)(*(t[0] if squeeze and t is not None else t for t in r))
 
     def fit_predict(self, data: torch.Tensor) -> torch.Tensor:
