@@ -20,6 +20,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 from torch.autograd.function import once_differentiable
 
 from . import (DTYPES, FK_ACT_GELU, FK_ACT_SILU, _call_logprob, _call_moe,
@@ -32,6 +33,13 @@ class TokenLogProbs(NamedTuple):
     entropy: torch.Tensor              # of the row's distribution
     top_ids: Optional[torch.Tensor]    # likeliest entries, int32, or None with top = 0
     top_logp: Optional[torch.Tensor]
+
+
+def _refuse_tangents(where: str, *tensors) -> None:
+    """Dual tensors do not require grad: without this their tangents would be dropped silently."""
+    for t in tensors:
+        if t is not None and unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{where} has no forward-mode derivative")
 
 
 def _forward(x, c, bias, ids, scale, top, rest=None):
@@ -99,10 +107,12 @@ def token_log_probs(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, *, scal
     ids (B, N); fp16, bf16 (d a multiple of 8) or fp32, x and c alike.  ids int32 or int64,
     negative: ignored (log probability 0, no gradient from it).  bias (K,) or (B, K);
     -inf masks an entry; a finite bias beyond 2^31 in magnitude counts as +-2^31.  top <= min(K, 28) likeliest entries, lowest index on ties.
-    logp, lse and entropy are fp32 and differentiable; top_ids and top_logp are not.
+    logp, lse and entropy are fp32 and differentiable (backward mode, once); top_ids and
+    top_logp are not.
     The backward pass can be captured into a CUDA graph while no eager autograd graph of
     the same leaves is alive; fk_logprob and fk_logprob_backward can be captured always.
     """
+    _refuse_tangents("token_log_probs", x, c, bias)
     if x.dim() < 1 or c.dim() not in (2, 3) or (c.dim() == 3 and x.dim() != 3):
         raise ValueError("x must be (..., d) and c (K, d), or x (B, N, d) and c (B, K, d)")
     lead = x.shape[:-1]
@@ -146,11 +156,12 @@ def expert_mixture(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_
     (softmax over all, lowest index on ties; renormalize: their weights sum to
     one) apply act(x gate^T) * (x up^T) with w_in (E, 2F, d), gate rows first,
     and w_out (E, d, F).  fp16 or bf16 throughout; d and F multiples of 8.
-    It has no backward pass: with gradients enabled, inputs that require them
-    are refused.
+    It has no derivatives: inputs that require gradients, with gradients enabled,
+    and dual tensors are refused.
     """
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+    _refuse_tangents("expert_mixture", x, router, w_in, w_out)
     if torch.is_grad_enabled() and (x.requires_grad or router.requires_grad or w_in.requires_grad
                                     or w_out.requires_grad):
         raise RuntimeError("expert_mixture has no backward pass: call it under torch.no_grad()")
