@@ -42,6 +42,12 @@ def _refuse_tangents(where: str, *tensors) -> None:
             raise RuntimeError(f"{where} has no forward-mode derivative")
 
 
+def _dense(t):
+    """Contiguous, and on the 16-byte border that 16-bit operands need: else a copy."""
+    t = t.contiguous()
+    return t.clone() if t.element_size() == 2 and t.data_ptr() % 16 else t
+
+
 def _forward(x, c, bias, ids, scale, top, rest=None):
     (B, N, d), K, dev = x.shape, c.shape[1], x.device
     if not x.is_cuda or x.dtype not in DTYPES:
@@ -104,8 +110,10 @@ def token_log_probs(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, *, scal
     """Log probabilities of ids under softmax(scale * x c^T + bias), with entropy and alternatives.
 
     x (..., d) with one table c (K, d) and ids (...), or batches x (B, N, d), c (B, K, d),
-    ids (B, N); fp16, bf16 (d a multiple of 8) or fp32, x and c alike.  ids int32 or int64,
-    negative: ignored (log probability 0, no gradient from it).  bias (K,) or (B, K);
+    ids (B, N); fp16, bf16 (d a multiple of 8) or fp32, x and c alike.  Strided tensors, and
+    16-bit ones that start off a 16-byte border, are copied.  ids int32 or int64,
+    negative: ignored (log probability 0, no gradient from it); K or more: the same, and
+    fk_device_error reports it.  bias (K,) or (B, K);
     -inf masks an entry; a finite bias beyond 2^31 in magnitude counts as +-2^31.  top <= min(K, 28) likeliest entries, lowest index on ties.
     logp, lse and entropy are fp32 and differentiable (backward mode, once); top_ids and
     top_logp are not.
@@ -128,7 +136,7 @@ def token_log_probs(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, *, scal
     if shared:
         x, c, ids = x.reshape(1, -1, x.shape[-1]), c.unsqueeze(0), ids.reshape(1, -1)
         bias = None if bias is None else bias.unsqueeze(0)
-    x, c, ids = x.contiguous(), c.contiguous(), ids.contiguous()
+    x, c, ids = _dense(x), _dense(c), ids.contiguous()
     bias = None if bias is None else bias.contiguous()
     if torch.is_grad_enabled() and (x.requires_grad or c.requires_grad or (bias is not None and bias.requires_grad)):
         out = _LogProbs.apply(x, c, bias, ids, float(scale), int(top))
@@ -155,7 +163,8 @@ def expert_mixture(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_
     x (..., d) and router (E, d) score the experts; each token's top_k experts
     (softmax over all, lowest index on ties; renormalize: their weights sum to
     one) apply act(x gate^T) * (x up^T) with w_in (E, 2F, d), gate rows first,
-    and w_out (E, d, F).  fp16 or bf16 throughout; d and F multiples of 8.
+    and w_out (E, d, F).  fp16 or bf16 throughout; d and F multiples of 8.  Strided
+    tensors, and those that start off a 16-byte border, are copied in every call.
     It has no derivatives: inputs that require gradients, with gradients enabled,
     and dual tensors are refused.
     """
@@ -177,8 +186,8 @@ def expert_mixture(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_
     if router.device != dev or w_in.device != dev or w_out.device != dev:
         raise ValueError(f"x is on {dev}, the weights on {router.device}, {w_in.device}, {w_out.device}")
     flat = x.dim() == 2
-    xs = (x if flat else x.reshape(-1, d)).contiguous()
-    router, w_in, w_out = router.contiguous(), w_in.contiguous(), w_out.contiguous()
+    xs = _dense(x if flat else x.reshape(-1, d))
+    router, w_in, w_out = _dense(router), _dense(w_in), _dense(w_out)
     T = xs.shape[0]
     y = torch.empty_like(xs)
     ids = xs.new_empty((T, k), dtype=torch.int32)
