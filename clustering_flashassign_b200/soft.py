@@ -64,10 +64,11 @@ def _forward(x, c, bias, ids, scale, top, rest=None):
         top_ids = x.new_empty((B, N, top), dtype=torch.int32)
         top_logp = x.new_empty((B, N, top), dtype=torch.float32)
         pi, pl = top_ids.data_ptr(), top_logp.data_ptr()
-    _call_logprob((B, N, K, d, DTYPES[x.dtype]), dev,
-                  (x.data_ptr(), c.data_ptr(), None if bias is None else bias.data_ptr(), scale, ids.data_ptr(),
-                   logp.data_ptr(), lse.data_ptr(), None if rest is None else rest.data_ptr(), entropy.data_ptr(),
-                   top, pi, pl))
+    if B:
+        _call_logprob((B, N, K, d, DTYPES[x.dtype]), dev,
+                      (x.data_ptr(), c.data_ptr(), None if bias is None else bias.data_ptr(), scale, ids.data_ptr(),
+                       logp.data_ptr(), lse.data_ptr(), None if rest is None else rest.data_ptr(),
+                       entropy.data_ptr(), top, pi, pl))
     return logp, lse, entropy, top_ids, top_logp
 
 
@@ -80,7 +81,8 @@ def _backward(ctx, dlogp, dlse, dentropy, *_):
     dx = torch.empty_like(x) if want[0] else None
     dc = torch.empty_like(c) if want[1] else None
     dbias = torch.empty_like(bias) if want[2] else None
-    fk_logprob_backward(x, c, ids, lse, entropy, *up, dx, dc, dbias, bias, ctx.scale, lse_rest=rest)
+    if x.shape[0]:
+        fk_logprob_backward(x, c, ids, lse, entropy, *up, dx, dc, dbias, bias, ctx.scale, lse_rest=rest)
     return dx, dc, dbias, None, None, None
 
 
