@@ -100,7 +100,7 @@ struct GradArgs {
 template <typename T, bool BIAS, bool SEG>
 struct GradEpi {
   using Args = GradArgs;
-  static constexpr bool kSeg = SEG;
+  static constexpr int kSeg = SEG ? tile::kSegBlocks : 0;
   static constexpr int kRegs = 152;
   const Args &a;
   const int r, lane;
@@ -219,10 +219,10 @@ struct StoreArgs {
   int add;                // partial sums add to what an earlier block of rows left
 };
 
-template <typename T, bool SEG>
+template <typename T, int SEG>
 struct StoreEpi {
   using Args = StoreArgs;
-  static constexpr bool kSeg = SEG;
+  static constexpr int kSeg = SEG;
   static constexpr int kRegs = 152;
   const Args &a;
   const int r, lane;
@@ -378,6 +378,18 @@ int launch_sum_parts(const float *part, int parts, long long n, int d, void *out
   return launched();
 }
 
+// dX or dC: a product with G, in segments where it is long.
+template <typename T, bool A_MN>
+int launch_product(const CUtensorMap &ta, const CUtensorMap &tb, const Plan &p, const StoreArgs &a, int fmt, int *err,
+                   cudaStream_t s) {
+  constexpr int kSeg = sizeof(T) == 4 ? tile::kSegBlocks : tile::kLongSegBlocks;
+  if constexpr (sizeof(T) == 2) {
+    if (cdiv((long long)p.pairs * p.kblocks, p.ksplits) <= kSeg)
+      return launch_tiles<StoreEpi<T, 0>, A_MN, true>(ta, tb, p, a, StoreEpi<T, 0>::smem_bytes(a.part), fmt, err, s);
+  }
+  return launch_tiles<StoreEpi<T, kSeg>, A_MN, true>(ta, tb, p, a, StoreEpi<T, kSeg>::smem_bytes(a.part), fmt, err, s);
+}
+
 // T: the gradients' type; G: the 16-bit type of the products' operands.
 template <typename T, typename G, bool BIAS>
 int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void *co, const void *cmul, const float *bias,
@@ -443,7 +455,7 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
         sa.batch_stride = m.N * m.d;
         sa.part = px.ksplits > 1 ? f.partx : nullptr;
         sa.slot = (long long)bn * nr * m.d;
-        FK_TRY((launch_tiles<StoreEpi<T, sizeof(T) == 4>, false, true>(tg, tcm, px, sa, StoreEpi<T, sizeof(T) == 4>::smem_bytes(sa.part), fmt, err, s)));
+        FK_TRY((launch_product<T, false>(tg, tcm, px, sa, fmt, err, s)));
         if (sa.part)
           FK_TRY(launch_sum_parts<T>(f.partx, px.ksplits, sa.slot, m.d, sa.out, s));
       }
@@ -470,7 +482,7 @@ int backward_typed(const Dims &m, const BwdSpace &f, const void *xo, const void 
         sa.part = f.w_parts ? f.partw : nullptr;
         sa.slot = (long long)bn * m.K * m.d;
         sa.add = r0 > 0;
-        FK_TRY((launch_tiles<StoreEpi<T, sizeof(T) == 4>, true, true>(tg, txm, pw, sa, StoreEpi<T, sizeof(T) == 4>::smem_bytes(sa.part), fmt, err, s)));
+        FK_TRY((launch_product<T, true>(tg, txm, pw, sa, fmt, err, s)));
         if (sa.part && r0 + nr >= m.N) {
           FK_TRY(launch_sum_parts<T>(f.partw, f.nr < m.N ? f.pw.ksplits : pw.ksplits, sa.slot, m.d, sa.out, s));
         }

@@ -22,7 +22,7 @@ namespace soft {
 template <bool BIAS, bool TOP, int LREG, bool SEG>
 struct StatEpi {
   using Args = StatArgs;
-  static constexpr bool kSeg = SEG;
+  static constexpr int kSeg = SEG ? tile::kSegBlocks : 0;
   static constexpr int kRegs = SEG && TOP ? 160 : 152;
   static constexpr int kSlots = 32 * tile::kEpiWarps;
   static constexpr int kCap = LREG ? LREG : 1;

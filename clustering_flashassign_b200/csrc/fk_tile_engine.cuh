@@ -67,9 +67,13 @@ __device__ __forceinline__ void take_registers() {
 constexpr uint32_t kABytes = kRows * kK * 2;
 // A chain of tcgen05 accumulations rounds towards zero at every step, which adds
 // up to a bias of about steps / 2 half-units of the result (3e-6 of it at 2048
-// terms).  Epilogues that ask for it (kSeg) get the contraction in segments of
-// 512 terms, summed in registers with rounding to nearest.
-constexpr int kSegBlocks = 8;
+// terms).  Epilogues that ask for it (kSeg) get the contraction in segments,
+// summed in registers with rounding to nearest: of 512 terms where fp32 results
+// hang on them, of 4096 (a bias of 2.6e-5 at most) where the result is rounded
+// to 16 bits.  One chain of 40000 terms was off by 1.3e-4, a quarter of fp16's
+// half step; segments of 1024 cost products of a training step 5%, these 1%
+// (N 4096, K 65536, d 2048).
+constexpr int kSegBlocks = 8, kLongSegBlocks = 64;
 constexpr int kMaxStages = 8;
 constexpr int kCtrlBytes = 256;  // barriers, TMEM address, abort flag
 
@@ -249,7 +253,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 
 // What an epilogue sees.  Epi provides
 //   struct Args                    kernel argument
-//   static constexpr bool kSeg     sum segments of the contraction in registers
+//   static constexpr int kSeg      K-blocks of a segment of the contraction, summed in registers; 0: one chain
 //   static constexpr int kRegs     registers of an epilogue thread, 152 or 160
 //   begin(const Unit &, row0)      before the unit's first tile
 //   skip(column)                   warp-uniform: nothing to do from this column on
@@ -385,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit w = unit_of(p, u);
         for (int ct = w.ct0; ct < w.ct1 && ok; ++ct) {
           for (int ks = w.k0; ks < w.k1 && ok; ++n) {
-            const int ke = Epi::kSeg && w.k1 - ks > kSegBlocks ? ks + kSegBlocks : w.k1;
+            const int ke = Epi::kSeg && w.k1 - ks > Epi::kSeg ? ks + Epi::kSeg : w.k1;
             const uint32_t buf = n & 1;
             if (!mbar_wait_spin(tempty(buf), ((n >> 1) & 1) ^ 1, abort_flag, err)) { ok = false; break; }
             tc_fence_after();
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long col0 = (long long)ct * kCols + first;
         const uint32_t lanes = tmem + first + ((uint32_t)(quad * 32) << 16);
         epi.prepare(col0, 96);
-        if constexpr (Epi::kSeg) {
+        if constexpr (Epi::kSeg > 0) {
           float sum[3][32];
           auto segment = [&](auto add) {
             const uint32_t buf = n & 1;
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
           };
           ok = segment(std::false_type{});
-          for (int ks = w.k0 + kSegBlocks; ks < w.k1 && ok; ks += kSegBlocks) ok = segment(std::true_type{});
+          for (int ks = w.k0 + Epi::kSeg; ks < w.k1 && ok; ks += Epi::kSeg) ok = segment(std::true_type{});
           if (ok) {
             // one copy of the epilogue's code: the sums move up instead
 #pragma unroll 1
