@@ -47,6 +47,9 @@ constexpr float kNegInf = -INFINITY;
 constexpr float kLowest = -256.f;
 // Columns beyond `top` that the running lists keep: the lists rank by fp32
 // scores, and the final order is settled in fp64 among top + kSpare columns.
+// Which columns are among them rests on the fp32 scores: more than kSpare others
+// within the rounding of the top-th may leave one of them out.  (An exact cut
+// would be a second product in fp64 for every row of such a table.)
 constexpr int kSpare = 2;
 constexpr int kMaxTop = 28;
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }

@@ -140,7 +140,9 @@ class FlashKMeans:
         trained centroids.  ids: the clusters asked for (default: the nearest one: predict(), or for
         fewer rows than centroids, which predict() refuses, the likeliest one).
         Returns soft.TokenLogProbs: logp of ids, entropy of the assignment, the `top` likeliest
-        clusters; lse omits -|x|^2 / temperature, which all clusters of a row share."""
+        clusters; lse omits -|x|^2 / temperature, which all clusters of a row share.  The scores are
+        2 x.c / temperature - |c|^2 / temperature in fp32: far from the origin these cancel, and
+        what is left is off by about 1e-6 |x| |c| / temperature (centre such data)."""
         from .soft import token_log_probs
         if self.centroids is None:
             raise RuntimeError("train the model first")

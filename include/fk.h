@@ -318,9 +318,12 @@ int fk_noalloc_device_error(fk_stream_t stream);
  *                1e-7), for the gradients; nullable
  *     logp     = s[b,n,ids[b,n]] - lse                (B, N) fp32
  *     entropy  = -sum_k p log p, p = exp(s - lse)     (B, N) fp32, nullable
- *     top_ids, top_logp  the `top` largest s, lowest index on ties (ordered by
- *                        their value in fp64), and their log probabilities
- *                        (B, N, top); NULL with top = 0
+ *     top_ids, top_logp  the `top` largest s, lowest index on ties, and their log
+ *                        probabilities (B, N, top); NULL with top = 0.  The
+ *                        top + 2 largest fp32 scores are kept and ordered by their
+ *                        value in fp64; where more columns than that lie within
+ *                        the fp32 score's rounding of the top-th, the fp32 scores
+ *                        decide which of these are in
  * The (B, N, K) scores are never stored.  For -t ||x - c||^2 in place of the
  * product pass scale = 2 t and bias = -t ||c||^2 (the row's own norm drops out).
  *
