@@ -62,7 +62,7 @@ __device__ __forceinline__ void exact_scores(const T *x, const T *c, const float
 #pragma unroll
     for (int o = LPR / 2; o; o >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
     s[i] *= (double)scale;
-    if (bias) s[i] = bias[k[i]] == kNegInf ? (double)kNegInf : s[i] + (double)clamp_bias(bias[k[i]]);
+    if (bias) s[i] = bias[k[i]] == kNegInf ? (double)kNegInf : s[i] + (double)bias[k[i]];
   }
 }
 

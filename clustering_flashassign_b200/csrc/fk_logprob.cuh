@@ -97,18 +97,20 @@ __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
-// A finite bias beyond 2^31 in magnitude counts as that: the lowest values of
+// A finite bias beyond 2.3e38 in magnitude counts as that: the lowest values of
 // bf16 and fp32, which programs mask with, would overflow times log2 e, and
-// 0 * inf is NaN.  What is masked so adds exactly nothing beside an ordinary
-// column, and lse and its rest still hold a row of nothing else (2^-16).
-constexpr float kMaxBias = 2147483648.f;
+// 0 * inf is NaN.  From 1e30 on, a column takes the path of masked ones, which
+// keeps differences from it finite; it adds exactly nothing beside an ordinary
+// column.
+constexpr float kMaxBias = 2.3e38f;
+constexpr float kMaskBias = 1e30f;
 __device__ __forceinline__ float clamp_bias(float b) {
   return fabsf(b) > kMaxBias && fabsf(b) < INFINITY ? copysignf(kMaxBias, b) : b;
 }
 
 // A warp's bias of its (at most four) 32-column chunks of a tile, times log2 e,
 // in shared memory; columns past the last count as masked.  `masked`: which of
-// the chunks hold a masked column.
+// the chunks hold a masked column, or one with a bias beyond kMaskBias.
 struct BiasTile {
   static constexpr int kFloats = 128;
   float *sb;
@@ -121,7 +123,7 @@ struct BiasTile {
       const long long col = col0 + i * stride + lane;
       const float b = col < K ? bias[col] : kNegInf;
       sb[i * 32 + lane] = clamp_bias(b) * kLog2e;
-      if (__any_sync(0xffffffffu, b == kNegInf)) masked |= 1u << i;
+      if (__any_sync(0xffffffffu, fabsf(b) > kMaskBias)) masked |= 1u << i;
     }
     __syncwarp();
   }
@@ -130,7 +132,7 @@ struct BiasTile {
 // The 32 scores of a thread's row in columns [col, col + 32), the warp's
 // chunk i: in base 2 with a bias, else the products as they are (the scale is
 // positive).  A bias of -inf masks its column whatever the product holds, and
-// columns past the last are masked; returns whether any of the 32 is.
+// columns past the last are masked; returns whether differences need a clamp.
 template <bool BIAS>
 __device__ __forceinline__ bool scores32(const float (&r)[32], float scale2, const BiasTile &bt, int i, long long col,
                                          long long K, float (&t)[32]) {

@@ -29,9 +29,12 @@ __global__ void __launch_bounds__(256)
   if (g.a == 0.f && l == 0.f && e == 0.f) g.id = -2;
   const double lse2 = ((double)v + (lse_rest ? (double)lse_rest[r] : 0.0)) * 1.4426950408889634;
   g.lse2 = (float)lse2;
-  // lse and lse_rest hold 2^-47 of the logarithm: where that is a unit and more
-  // (scores of 10^14), nothing below g.lse2 is known
-  const float lo = fabs(lse2) < 140737488355328.0 ? (float)(lse2 - (double)g.lse2) : 0.f, f = exp2f(-lo);
+  // lse and lse_rest hold 2^-47 of the logarithm.  Beyond 2^31, scores are 256
+  // apart or equal: the row is even over its largest ones, g.lse2 is their score
+  // and the logarithm of their number is the entropy.
+  float lo = v == kNegInf ? 0.f : (float)(lse2 - (double)g.lse2);
+  if (fabs(lse2) >= 2147483648.0) lo = entropy ? entropy[r] * kLog2e : fabs(lse2) < 140737488355328.0 ? lo : 0.f;
+  const float f = exp2f(-lo);
   g.c1 = f * (l - g.a - e * (dent ? entropy[r] : 0.f) + e * kLn2 * lo);
   g.c2 = -f * e * kLn2;
   if (lane == 0) {

@@ -116,7 +116,7 @@ def token_log_probs(x: torch.Tensor, c: torch.Tensor, ids: torch.Tensor, *, scal
     16-bit ones that start off a 16-byte border, are copied.  ids int32 or int64,
     negative: ignored (log probability 0, no gradient from it); K or more: the same, and
     fk_device_error reports it.  bias (K,) or (B, K);
-    -inf masks an entry; a finite bias beyond 2^31 in magnitude counts as +-2^31.  top <= min(K, 28) likeliest entries, lowest index on ties
+    -inf masks an entry; a finite bias beyond 2.3e38 in magnitude counts as that.  top <= min(K, 28) likeliest entries, lowest index on ties
     (ordered by fp64 scores among the top + 2 largest fp32 scores).
     logp, lse and entropy are fp32 and differentiable (backward mode, once); top_ids and
     top_logp are not.

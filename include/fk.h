@@ -329,8 +329,8 @@ int fk_noalloc_device_error(fk_stream_t stream);
  *
  * shape: N >= 0 (K may exceed N), d <= 2^20, otherwise fk_assign's rules.
  * scale positive and finite.  bias fp32 (B, K), nullable; an entry of -inf masks
- * its column whatever the table's row holds.  A finite bias beyond 2^31 in
- * magnitude counts as +-2^31: the lowest values of bf16 and fp32 leave nothing of
+ * its column whatever the table's row holds.  A finite bias beyond 2.3e38 in
+ * magnitude counts as +-2.3e38: the lowest values of bf16 and fp32 leave nothing of
  * a column beside an ordinary one, and rows of nothing else stay finite.
  * 0 <= top <= min(K, 28).  A negative id is ignored: its logp is 0.  An id of K or
  * more does the same and records FK_EINVAL in the device error word.  A row whose
@@ -356,8 +356,8 @@ int fk_logprob_workspace(const fk_shape *shape, int top, long long *bytes);
  *     dc   = scale G^T x      (B, K, d) in the inputs' type
  *     dbias = sum_n G         (B, K) fp32
  * Each result is nullable (not computed).  lse and entropy are the forward
- * call's (entropy only with dentropy; lse_rest nullable: p is then off by lse's
- * rounding).  Ignored rows get nothing from dlogp; a
+ * call's (entropy needed with dentropy; without it p is not known in rows whose
+ * scores tie beyond 2^31; lse_rest nullable: p is then off by lse's rounding).  Ignored rows get nothing from dlogp; a
  * row without any upstream gradient gets zeros and contributes nothing, whatever
  * it holds; masked columns get zeros and contribute nothing.  Results are
  * bit-reproducible: no atomics touch them.  Workspace as in fk_logprob; it holds

@@ -1,7 +1,7 @@
 """Finite masks, and scores so large that fp32 holds whole numbers only.
 
-A bias of 2^31 or more in magnitude counts as that (a score in base 2 must not
-overflow); beside an ordinary column either contributes exactly nothing.
+A bias beyond 2.3e38 in magnitude counts as that (a score in base 2 must not overflow);
+beside an ordinary column either contributes exactly nothing.
 """
 import math
 
@@ -61,10 +61,10 @@ def test_rows_whose_every_column_has_the_lowest_bias_are_even(N, dtype, value):
     # log2 of the sum (1 ulp of 8 to 16), its conversion, and the exponentials
     assert ((r.logp[1] + math.log(K))[valid].abs() <= 16 * U * math.log(K)).all()
     assert ((r.entropy[1] - math.log(K)).abs() <= 16 * U * math.log(K)).all()
-    count = max(value, -2.0 ** 31)
+    count = max(value, -2.3e38)
     assert ((r.lse[1] - count).abs() <= 2 * U * abs(count)).all()
     assert ((r.top_logp[1] + math.log(K)).abs() <= 16 * U * math.log(K)).all()
-    # p from lse: held to 2^-47 of its size beside the rest, 3e9 in base 2
+    # p from lse: held to 2^-47 of its size (up to 2^31 in base 2), beyond that from the entropy
     rel = 2.0 ** -15
     G = -torch.ones(N, K, device="cuda", dtype=torch.float64) / K
     G.scatter_add_(1, ids[1].clamp(min=0).long().unsqueeze(1), torch.ones(N, 1, device="cuda", dtype=torch.float64))
@@ -108,6 +108,32 @@ def test_equal_biases_beyond_the_range_of_scores(shift, N, top):
         assert ((r.top_logp + math.log(K)).abs() <= 16 * U * math.log(K)).all()
     count = torch.bincount(ids[0].long(), minlength=K).double()
     want = count - N / K
-    # p from lse, held to 2^-47 of its size (at most 3e9 in base 2), and fp32 sums of N terms
+    # p from lse, held to 2^-47 of its size (up to 2^31 in base 2), and fp32 sums of N terms
     assert ((db[0].double() - want).abs() <= N / K * 2.0 ** -15 + (count + N / K) * (N / 32 + 8) * U).all()
     assert (dc == 0).all()
+
+
+@pytest.mark.parametrize("temperature", [1.0, 1e-3, 1e-6, 1e-9, 1e-12, 1e-20])
+@pytest.mark.parametrize("N", [40, 5000])
+def test_low_temperatures_pick_the_nearest_centroid(N, temperature):
+    """Large products and a large bias that nearly cancel: neither may be cut on its own."""
+    from clustering_flashassign_b200.soft import token_log_probs
+    K, d = 200, 48
+    g = torch.Generator(device="cuda").manual_seed(N)
+    c = torch.randn(1, K, d, generator=g, device="cuda")
+    c *= 1 + 3 * torch.rand(1, K, 1, generator=g, device="cuda")  # of lengths 7 to 28: x.c alone misleads
+    near = torch.randint(0, K, (N,), generator=g, device="cuda")
+    x = (c[:, near] + 0.05 * torch.randn(1, N, d, generator=g, device="cuda")).contiguous()
+    bias = -c.square().sum(-1) / temperature
+    leaf = x.clone().requires_grad_(True)
+    r = token_log_probs(leaf, c, near.int().unsqueeze(0), scale=2 / temperature, bias=bias, top=2)
+    d2 = torch.cdist(x.double(), c.double()).square()
+    assert (d2.argmin(-1)[0] == near).all()
+    assert torch.equal(r.top_ids[0, :, 0].long(), near)
+    # every other centroid is at least 20 further off (squared): p < 200 e^-20
+    gap = d2.topk(2, dim=-1, largest=False).values
+    assert float((gap[..., 1] - gap[..., 0]).min()) > 20
+    assert (r.logp.abs() <= 200 * math.exp(-20)).all() and (r.entropy.abs() <= 40 * 200 * math.exp(-20) + 16 * U).all()
+    dx = torch.autograd.grad(r.logp.sum(), leaf)[0]
+    # scale (1 - p) |c| with 1 - p off by two exponentials (2^-20)
+    assert (dx.abs() <= 2 / temperature * (200 * math.exp(-20) + 2.0 ** -20) * 2 * float(c.abs().max())).all()
