@@ -41,7 +41,8 @@ __global__ void __launch_bounds__(256)
     out[r] = g;
     // |p (log p + H)| <= max(1 / e, log K) <= log K + 1
     const float big = fabsf(g.a) + fabsf(l) + fabsf(e) * (logf((float)K) + 1.f);
-    if (bound && big > 0.f) atomicMax(bound, __float_as_uint(big));
+    // a row whose gradient overflowed does not take the others' scale
+    if (bound && big > 0.f && big < INFINITY) atomicMax(bound, __float_as_uint(big));
   }
   copy_row<T>(x, r, rows_per_b, d, dp, g.id == -2, xs, lane);
 }
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(256)
 // The power of two that brings `bound` to [2^13, 2^14), within [2^-100, 2^100].
 __device__ __forceinline__ float grad_scale(unsigned bound) {
   const float b = __uint_as_float(bound);
-  if (!(b > 0.f) || !(b < INFINITY)) return 1.f;
+  if (!(b > 0.f)) return 1.f;
   int e = 13 - ilogbf(b);
   e = e < -100 ? -100 : e > 100 ? 100 : e;
   return ldexpf(1.f, e);
