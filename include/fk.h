@@ -360,8 +360,12 @@ int fk_logprob_workspace(const fk_shape *shape, int top, long long *bytes);
  * scores tie beyond 2^31; lse_rest nullable: p is then off by lse's rounding).  Ignored rows get nothing from dlogp; a
  * row without any upstream gradient gets zeros and contributes nothing, whatever
  * it holds; masked columns get zeros and contribute nothing.  Results are
- * bit-reproducible: no atomics touch them.  Workspace as in fk_logprob; it holds
- * G in the inputs' type for a block of rows, 4 GiB at most (256 rows at least).
+ * bit-reproducible: no atomics touch them.  fp16 holds G at one power-of-two scale
+ * per call, which brings its largest possible value to 2^13 or more: values below
+ * 2^-28 of that lose digits, below 2^-38 they vanish.  Rows whose upstream
+ * gradients are 10^6 times smaller than the call's largest belong in a call of
+ * their own, or in bf16.  Workspace as in fk_logprob; it holds G in the inputs'
+ * type for a block of rows, 4 GiB at most (256 rows at least).
  */
 int fk_logprob_backward(const fk_shape *shape, const void *x, const void *c, const float *bias, float scale,
                         const int32_t *ids, const float *lse, const float *lse_rest, const float *entropy,
