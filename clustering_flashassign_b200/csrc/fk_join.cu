@@ -148,7 +148,7 @@ __device__ __forceinline__ RowStat row_stat(float m, float s, float u) {
   r.none = m == kNegInf && s == 0.f;
   r.nan = !(s == s);
   r.hs = u / s;
-  if (s > 0.f && s < INFINITY && fabsf(m) < 8388608.f) {
+  if (s > 0.f && s < INFINITY && fabsf(m) < kCoarse) {
     const int e = ilogbf(s);
     r.m = m + (float)e;
     r.sig = scalbnf(s, -e);
@@ -168,7 +168,7 @@ __device__ __forceinline__ RowStat row_stat(float m, float s, float u) {
 // (2^-22 of it) cancels in the difference instead of standing beside a small result.
 __device__ __forceinline__ float stored_logp(const JoinArgs &a, const RowStat &q, float v) {
   if (q.none || (v == kNegInf && !q.nan)) return kNegInf;
-  const float rel = a.bias ? v - q.m : fmaf(v, a.scale * kLog2e, -q.m);
+  const float rel = fabsf(q.m) >= kCoarse ? __fmul_rn(v, a.unit2) - q.m : fmaf(v, a.unit2, -q.m);
   const float e = ex2(rel);
   if (e + e > q.sig && q.sig < INFINITY) return -log1pf(fmaxf(q.sig - e, 0.f) / e);
   return -at_least_0((q.ls - rel) * kLn2);
@@ -486,9 +486,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join_block(const JoinArgs a
   }
 }
 
-// Many rows of few parts: a thread per row.  LL = 0: statistics only.
+// Many rows of few parts: a thread per row.  LL = 0: statistics only.  Three CTAs an
+// SM with the shortest lists: three registers more cost the third, and 604800 rows 2%.
 template <typename T, int LL>
-__global__ void __launch_bounds__(256) k_join_rows(const JoinArgs a) {
+__global__ void __launch_bounds__(256, LL <= 4 ? 3 : 1) k_join_rows(const JoinArgs a) {
   pdl_wait();
   constexpr int C = LL ? LL : 1;
   const int lane = threadIdx.x & 31;

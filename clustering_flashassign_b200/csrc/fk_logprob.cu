@@ -120,7 +120,7 @@ int fk_logprob(const fk_shape *shape, const void *x, const void *c, const float 
   FK_TRY((bias ? launch_scores_bias : launch_scores)(tx, tc, f, a, bf ? 1 : 0, err, s));
   JoinArgs j = {};
   j.part = f.part, j.top_v = f.top_v, j.top_i = f.top_i;
-  j.ids = ids, j.x = x, j.c = c, j.bias = bias, j.scale = scale;
+  j.ids = ids, j.x = x, j.c = c, j.bias = bias, j.scale = scale, j.unit2 = bias ? 1.f : scale * kLog2e;
   j.rows = m.B * m.N, j.N = m.N, j.K = m.K, j.d = m.d;
   j.parts = a.parts, j.L = f.L, j.cands = top ? std::min(m.K, top + kSpare) : 0, j.top = top;
   j.logp = logp, j.lse = lse, j.lse_rest = lse_rest, j.entropy = entropy, j.top_logp = top_logp, j.top_ids = top_ids;

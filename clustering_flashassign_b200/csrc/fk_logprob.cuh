@@ -166,6 +166,12 @@ __device__ __forceinline__ bool scores32(const float (&r)[32], float scale2, con
   }
 }
 
+// References from here on are no longer exact to a unit, and the rounding of a
+// product times the scale (without a bias it is not rounded before the reference
+// is subtracted) would show as a difference from its own maximum, up to 2^128 and
+// more in the sum: such products are rounded first, wherever they are used.
+constexpr float kCoarse = 8388608.f;
+
 // One row's coefficients: G_k = p (c1 + c2 log2 p) + a 1[k = id], p = 2^(t_k - lse2).
 // lse in base 2 is lse2 and a remainder below its rounding; c1 and c2 carry it.
 struct RowGrad {
@@ -197,6 +203,7 @@ struct JoinArgs {
   const void *x, *c;
   const float *bias;
   float scale;
+  float unit2;  // of the stored scores in base 2: scale * log2 e, with a bias 1
   long long rows, N, K;
   int d, parts, L, cands, top;  // L: length of a partial list; cands = min(K, top + kSpare)
   bool vec;  // rows of x and c can be read 16 bytes at a time
@@ -242,7 +249,8 @@ inline int check_soft(const fk_shape *shape, float scale) {
   // row numbers of the last tile's empty rows are ints too
   if (shape->N > 0x7fffffffLL - 512) return set_error(FK_EUNSUPPORTED, "N above 2^31 - 513");
   if (shape->d > (1 << 20)) return set_error(FK_EUNSUPPORTED, "d above 2^20");
-  if (!(scale > 0.f) || !(scale < INFINITY)) return set_error(FK_EINVAL, "scale must be positive and finite");
+  if (!(scale > 0.f) || !(scale * kLog2e < INFINITY))
+    return set_error(FK_EINVAL, "scale must be positive and finite (below 2.3e38)");
   return FK_OK;
 }
 

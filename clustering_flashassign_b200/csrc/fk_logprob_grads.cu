@@ -146,7 +146,13 @@ struct GradEpi {
     {
       float v[32];
       const bool some_masked = scores32<BIAS>(acc, a.scale2, bt, i, col, a.K, v);
-      const float2 nl = make_float2(-q.lse2, -q.lse2), sc = make_float2(a.scale2, a.scale2);
+      const bool coarse = !BIAS && fabsf(q.lse2) >= kCoarse;
+      if (!BIAS && __any_sync(0xffffffffu, coarse)) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = coarse ? __fmul_rn(v[j], a.scale2) : v[j];
+      }
+      const float s1 = coarse ? 1.f : a.scale2;
+      const float2 nl = make_float2(-q.lse2, -q.lse2), sc = make_float2(s1, s1);
       const float2 c1 = make_float2(q.c1, q.c1), c2 = make_float2(q.c2, q.c2);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {

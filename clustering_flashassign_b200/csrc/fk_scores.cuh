@@ -135,7 +135,7 @@ struct StatEpi {
       g[q] = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), fmaxf(v[6], v[7]));
     }
     const float cm = max3(fmaxf(g[0], g[1]), g[2], g[3]);
-    const float c2 = BIAS ? cm : cm * a.scale2;
+    const float c2 = BIAS ? cm : __fmul_rn(cm, a.scale2);
     if (c2 > m + 2.f) {  // always the case for the first finite chunk
       const float up = ceilf(c2);
       if (m != kNegInf) {
@@ -148,7 +148,8 @@ struct StatEpi {
     const float ms = m == kNegInf ? 0.f : m;
     const float2 ref = make_float2(-ms, -ms), sc = make_float2(a.scale2, a.scale2);
     float2 s2[2] = {}, u2[2] = {};
-    if (!some_masked) {
+    const bool coarse = !BIAS && fabsf(ms) >= kCoarse;
+    if (!some_masked && !coarse) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float2 v = make_float2(t[2 * j], t[2 * j + 1]);
@@ -161,7 +162,8 @@ struct StatEpi {
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float2 v = make_float2(t[2 * j], t[2 * j + 1]);
-        const float2 dd = BIAS ? __fadd2_rn(v, ref) : __ffma2_rn(v, sc, ref);
+        float2 dd = BIAS ? __fadd2_rn(v, ref) : __ffma2_rn(v, sc, ref);
+        if (coarse) dd = make_float2(__fmul_rn(v.x, a.scale2) - ms, __fmul_rn(v.y, a.scale2) - ms);
         const float2 e = make_float2(ex2(dd.x), ex2(dd.y));
         s2[j & 1] = __fadd2_rn(s2[j & 1], e);
         u2[j & 1] = __ffma2_rn(e, make_float2(fmaxf(dd.x, kLowest), fmaxf(dd.y, kLowest)), u2[j & 1]);

@@ -328,7 +328,7 @@ int fk_noalloc_device_error(fk_stream_t stream);
  * product pass scale = 2 t and bias = -t ||c||^2 (the row's own norm drops out).
  *
  * shape: N >= 0 (K may exceed N), d <= 2^20, otherwise fk_assign's rules.
- * scale positive and finite.  bias fp32 (B, K), nullable; an entry of -inf masks
+ * scale positive and below 2.3e38.  bias fp32 (B, K), nullable; an entry of -inf masks
  * its column whatever the table's row holds.  A finite bias beyond 2.3e38 in
  * magnitude counts as +-2.3e38: the lowest values of bf16 and fp32 leave nothing of
  * a column beside an ordinary one, and rows of nothing else stay finite.
