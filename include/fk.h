@@ -336,7 +336,7 @@ int fk_noalloc_device_error(fk_stream_t stream);
  * more does the same and records FK_EINVAL in the device error word.  A row whose
  * every column is masked has lse = logp = -inf and entropy 0; masked columns fill
  * up top, lowest index first.  fp32 inputs are multiplied as three bf16 parts each
- * (about 2^-24).
+ * (about 2^-24; values beyond bf16's largest, 3.39e38, count as infinite).
  *
  * workspace: device memory of the caller's (16-byte aligned, at least
  * fk_logprob_workspace bytes), in use until the call's work on `stream` is
